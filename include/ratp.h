@@ -323,6 +323,45 @@ int ratp_dilated_attn_prefill_per_sample_ws(const void* q, const void* hk, const
                                             void* stream);
 
 /* ------------------------------------------------------------------------
+ * RMS norm of every head of q and k with the rotary position in the same pass
+ * (the step between a layer's projections and its mixer; the write-up does
+ * not describe it, layers that feed this mixer have it).
+ *
+ * For every head row x of q and of k:
+ *   y_c = x_c / sqrt(mean_c(x_c^2) + eps) * weight_c, then pair i < rot/2 of
+ *   the first rot channels turns by pos * inv_freq[i]:
+ *   (u, v) -> (u cos - v sin, v cos + u sin).
+ * Pair i is channels (i, i + rot/2), or (2i, 2i + 1) with interleaved != 0.
+ * Arithmetic is fp32, the angle fp64; one rounding to dtype at the end.
+ *
+ * q, k, q_out, k_out: views of dtype; element (b, t, h, c) of a view is
+ *   data[b*stride_b + t*stride_t + h*stride_h + c].  Strides count elements,
+ *   are not negative, and keep every row 16-byte aligned (so q and k may be
+ *   read out of one fused projection).  A decode token is T = 1.  An output
+ *   view may be the input view itself (same data and strides: in place);
+ *   otherwise outputs overlap neither inputs nor each other.  A tensor with
+ *   heads == 0 is left out.
+ * q_weight, k_weight: fp32 [Dh] gains; NULL = 1.
+ * inv_freq: fp32 [rot/2]; may be NULL when rot == 0 (norm only).
+ * positions: NULL (token t sits at position t); int32 [B] (position of token
+ *   0 of each sequence, e.g. a cache's len: token t sits at positions[b] + t);
+ *   or int32 [B][T] with positions_per_token != 0.  Any int32 value.
+ * Errors: ARG (null pointer, negative size or stride, bad dtype, eps < 0 or
+ *   not finite), SHAPE (Dh not 64/128, rot not a multiple of 16 in 0..Dh, too
+ *   many heads), ALIGN.  B or T == 0 is a no-op.
+ * ---------------------------------------------------------------------- */
+typedef struct ratp_view {
+  void* data;
+  int64_t stride_b, stride_t, stride_h;
+  int32_t heads;
+} ratp_view;
+
+int ratp_qk_norm_rope(const ratp_view* q, const ratp_view* k, const ratp_view* q_out, const ratp_view* k_out,
+                      const float* q_weight, const float* k_weight, const float* inv_freq,
+                      const int32_t* positions, int positions_per_token,
+                      int B, int T, int Dh, int rot, int interleaved, float eps, int dtype, void* stream);
+
+/* ------------------------------------------------------------------------
  * D-compressed KV cache and decode (RAT+ abstract: the KV cache shrinks by D).
  *
  * Layout (all bf16 rows of Dh elements):
@@ -356,6 +395,10 @@ typedef struct ratp_cache {
   int32_t reset_L;      /* chunk-local recurrence block (0 = full sequence); set by
                            ratp_cache_set_chunk_local */
   int32_t window_L;     /* fixed look-back window (0 = none); set by ratp_cache_set_window */
+  int32_t kv_bits;      /* bits a channel of the dilated rows: 16 (bf16; 0 reads as 16) or 4
+                           (ratp_cache_init_q4: Kc, Vc hold codes, Kp, Vp their parameters) */
+  void* Kp;             /* 4-bit rows: uint32 [B * rows_per_b][Dh / 32], scale (bf16, low half) */
+  void* Vp;             /* and minimum (bf16, high half) of each 32 channels; else NULL */
   uint8_t dense[RATP_MAX_HEADS];
 } ratp_cache;
 
@@ -369,6 +412,32 @@ int ratp_cache_bytes(int B, int H, int Dh, int T_max, int D, int W,
 int ratp_cache_init(ratp_cache* c, void* buffer, size_t bytes,
                     int B, int H, int Dh, int T_max, int D, int W,
                     const uint8_t* head_mask, void* stream);
+
+/* The same cache with its dilated rows held in 4 bits a channel (the write-up's
+ * section 8.2 names low-bit quantisation of the compressed cache as the next
+ * step).  Each row is kept in groups of 32 channels; a group keeps its minimum
+ * m, the step s = bf16((max - m) / 15) and the codes n = round((x - m) / s) in
+ * 0..15 (round half to even; 0 where s == 0), and stands for m + n s, so that
+ * a row of Dh channels takes Dh/2 + Dh/8 bytes instead of 2 Dh.  Code words:
+ * uint32 [B * rows_per_b][Dh / 8] in Kc / Vc; channel c of a word's 8 sits in
+ * nibble c/2 + 4 (c mod 2).  The window ring stays bf16 and the recurrent state
+ * fp32, so the last W positions are read as they are.
+ * Values must be finite and max - m within fp32.
+ * Every other entry point takes such a cache as it takes a bf16 one
+ * (ratp_cache_pack quantises; ratp_decode_step quantises the row it appends
+ * and attends to the held values; ratp_decode_step_layers mixes both kinds).
+ * Arguments and errors as ratp_cache_bytes / ratp_cache_init. */
+int ratp_cache_bytes_q4(int B, int H, int Dh, int T_max, int D, int W,
+                        const uint8_t* head_mask, size_t* bytes);
+int ratp_cache_init_q4(ratp_cache* c, void* buffer, size_t bytes,
+                       int B, int H, int Dh, int T_max, int D, int W,
+                       const uint8_t* head_mask, void* stream);
+
+/* The values that a 4-bit cache's dilated rows stand for (m + n s, fp32):
+ * k, v: device fp32 [B][rows_per_b][Dh], 16-byte aligned; either may be NULL
+ * (left out).  Rows that neither a pack nor a step has written hold no
+ * meaningful value.  Errors: ARG (null c, a bf16 cache), ALIGN. */
+int ratp_cache_read_q4(const ratp_cache* c, float* k, float* v, void* stream);
 
 /* Prefill -> decode hand-off: copies the dilated rows of hk, hv (bf16
  * [B][T][H][Dh], T <= T_max) into Kc/Vc, the last min(W, T) positions into

@@ -22,6 +22,7 @@ from ._binding import (  # noqa: F401
     load_library,
     prefill_fused,
     prefill_fused_workspace,
+    qk_norm_rope,
     scan_prefill,
     scan_prefill_kv,
     scan_prefill_kv_noalloc,

@@ -42,7 +42,8 @@ class CacheStruct(ctypes.Structure):
         ("B", ctypes.c_int32), ("H", ctypes.c_int32), ("Dh", ctypes.c_int32),
         ("T_max", ctypes.c_int32), ("D", ctypes.c_int32), ("W", ctypes.c_int32),
         ("split_keys", ctypes.c_int32), ("max_splits", ctypes.c_int32),
-        ("reset_L", ctypes.c_int32), ("window_L", ctypes.c_int32),
+        ("reset_L", ctypes.c_int32), ("window_L", ctypes.c_int32), ("kv_bits", ctypes.c_int32),
+        ("Kp", ctypes.c_void_p), ("Vp", ctypes.c_void_p),
         ("dense", ctypes.c_uint8 * MAX_HEADS),
     ]
 
@@ -53,6 +54,15 @@ class DecodeLayerStruct(ctypes.Structure):
         ("q", ctypes.c_void_p), ("xk", ctypes.c_void_p), ("xv", ctypes.c_void_p),
         ("g", ctypes.c_void_p), ("state", ctypes.c_void_p),
         ("cache", ctypes.POINTER(CacheStruct)), ("o", ctypes.c_void_p),
+    ]
+
+
+class ViewStruct(ctypes.Structure):
+    """Mirror of ``struct ratp_view``."""
+    _fields_ = [
+        ("data", ctypes.c_void_p),
+        ("stride_b", ctypes.c_int64), ("stride_t", ctypes.c_int64), ("stride_h", ctypes.c_int64),
+        ("heads", ctypes.c_int32),
     ]
 
 
@@ -81,6 +91,10 @@ _SIGS = {
     "ratp_dilated_attn_prefill_per_sample_ws": ([_P, _P, _P, _P, _I, _I, _I, _I, _P, _I, _P, _I, _P, _P], _I),
     "ratp_prefill_fused_workspace_bytes": ([_I, _I, _I, _I, ctypes.POINTER(_SZ)], _I),
     "ratp_prefill_fused": ([_P, _P, _P, _P, _P, _P, _P, _P, _I, _I, _I, _I, _I, _I, _P, _I, _P, _SZ, _P], _I),
+    "ratp_qk_norm_rope": ([ctypes.POINTER(ViewStruct)] * 4 + [_P] * 4 + [_I] * 6 + [ctypes.c_float, _I, _P], _I),
+    "ratp_cache_bytes_q4": ([_I, _I, _I, _I, _I, _I, _P, ctypes.POINTER(_SZ)], _I),
+    "ratp_cache_init_q4": ([ctypes.POINTER(CacheStruct), _P, _SZ, _I, _I, _I, _I, _I, _I, _P, _P], _I),
+    "ratp_cache_read_q4": ([ctypes.POINTER(CacheStruct), _P, _P, _P], _I),
     "ratp_cache_bytes": ([_I, _I, _I, _I, _I, _I, _P, ctypes.POINTER(_SZ)], _I),
     "ratp_cache_init": ([ctypes.POINTER(CacheStruct), _P, _SZ, _I, _I, _I, _I, _I, _I, _P, _P], _I),
     "ratp_cache_pack": ([ctypes.POINTER(CacheStruct), _P, _P, _I, _P], _I),
@@ -398,6 +412,95 @@ def prefill_fused(q, xk, xv, g, D, W=0, head_mask=None, hk=None, hv=None, out=No
     return out, hk, hv
 
 
+def _head_rows(t, name, dtype, device):
+    """(B, T, H, Dh, strides of b, t, h) of a [B, T, H, Dh] or [B, H, Dh] view
+    whose channels are contiguous."""
+    if not isinstance(t, torch.Tensor) or not t.is_cuda:
+        raise ValueError("%s must be a CUDA tensor" % name)
+    if t.dtype != dtype or t.device != device:
+        raise ValueError("%s must be %s on %s, got %s on %s" % (name, dtype, device, t.dtype, t.device))
+    if t.dim() == 4:
+        (B, T, H, Dh), (sb, st, sh, sc) = t.shape, t.stride()
+    elif t.dim() == 3:
+        (B, H, Dh), (sb, sh, sc), T, st = t.shape, t.stride(), 1, 0
+    else:
+        raise ValueError("%s must be [B, T, H, Dh] or [B, H, Dh]" % name)
+    if sc != 1 and Dh > 1:
+        raise ValueError("%s: channels must be contiguous" % name)
+    # the stride of a dimension of one element is never used
+    return B, T, H, Dh, sb if B > 1 else 0, st if T > 1 else 0, sh if H > 1 else 0
+
+
+def qk_norm_rope(q, k, q_weight, k_weight, inv_freq, positions=None, eps=1e-6, interleaved=False,
+                 q_out=None, k_out=None):
+    """(q_out, k_out): RMS norm of every head of q and k, times the gain of its
+    channel, turned by its token's rotary position, in one pass.
+
+    q, k: [B, T, H, Dh] (or [B, H, Dh], one token per sequence), bf16 or fp32,
+    Dh 64 or 128; their head counts may differ, and either may be None.  Any
+    strides that keep a head's channels contiguous and its row 16-byte aligned
+    do, so both may be views of one fused projection.
+    q_weight, k_weight: fp32 [Dh] gains, or None.
+    inv_freq: fp32 [rot / 2], rot <= Dh a multiple of 16: the first rot
+    channels turn by position * inv_freq (the angle is taken in fp64); None
+    leaves the rotation out.  Pair i is channels (i, i + rot/2), or (2i, 2i+1)
+    with ``interleaved``.
+    positions: None (0 .. T-1), int32 [B] (the position of each sequence's
+    first token here, e.g. ``KVCache.lengths()``) or int32 [B, T].
+    q_out, k_out: outputs; q and k themselves work in place."""
+    lib = load_library()
+    if q is None and k is None:
+        raise ValueError("q and k are both None")
+    ref = k if q is None else q
+    if not isinstance(ref, torch.Tensor) or not ref.is_cuda:
+        raise ValueError("q and k must be CUDA tensors")
+    dt, dev = ref.dtype, ref.device
+    if dt not in _DTYPE:
+        raise ValueError("unsupported dtype %s" % dt)
+    views, outs, shape = [], [], None
+    for x, out, nm in ((q, q_out, "q"), (k, k_out, "k")):
+        if x is None:
+            views.append((ViewStruct(), ViewStruct()))
+            outs.append(None)
+            continue
+        B, T, H, Dh, sb, st, sh = _head_rows(x, nm, dt, dev)
+        if shape is None:
+            shape = (x.dim(), B, T, Dh)
+        elif shape != (x.dim(), B, T, Dh):
+            raise ValueError("q and k must agree in batch, tokens and head size")
+        if out is None:
+            out = torch.empty(x.shape, dtype=dt, device=dev)
+        elif out.shape != x.shape:
+            raise ValueError("%s_out must have the shape of %s" % (nm, nm))
+        _, _, _, _, ob, ot, oh = _head_rows(out, nm + "_out", dt, dev)
+        views.append((ViewStruct(x.data_ptr(), sb, st, sh, H), ViewStruct(out.data_ptr(), ob, ot, oh, H)))
+        outs.append(out)
+    _, B, T, Dh = shape
+    for w, nm in ((q_weight, "q_weight"), (k_weight, "k_weight")):
+        if w is not None:
+            _need(w, nm, torch.float32)
+            if w.shape != (Dh,) or w.device != dev:
+                raise ValueError("%s must be [Dh] on %s" % (nm, dev))
+    rot = 0
+    if inv_freq is not None:
+        _need(inv_freq, "inv_freq", torch.float32)
+        if inv_freq.dim() != 1 or inv_freq.device != dev:
+            raise ValueError("inv_freq must be [rot / 2] on %s" % dev)
+        rot = 2 * inv_freq.numel()
+    per_token = 0
+    if positions is not None:
+        _need(positions, "positions", torch.int32)
+        if positions.device != dev or tuple(positions.shape) not in ((B,), (B, T)):
+            raise ValueError("positions must be int32 [B] or [B, T] on %s" % dev)
+        per_token = 1 if positions.dim() == 2 else 0
+    with torch.cuda.device(dev):
+        _check("ratp_qk_norm_rope", lib.ratp_qk_norm_rope(
+            views[0][0], views[1][0], views[0][1], views[1][1], _ptr(q_weight if q is not None else None),
+            _ptr(k_weight if k is not None else None), _ptr(inv_freq), _ptr(positions), per_token, B, T, Dh, rot,
+            1 if interleaved else 0, float(eps), _DTYPE[dt], _stream(ref)))
+    return tuple(outs)
+
+
 def last_error(device=None):
     """Synchronise and raise if any kernel recorded a device-side error."""
     lib = load_library()
@@ -423,17 +526,27 @@ def sm_count() -> int:
 class KVCache:
     """D-compressed KV cache for decode (one device buffer, see ``ratp.h``)."""
 
-    def __init__(self, B, H, Dh, T_max, D, W=0, head_mask=None, device="cuda", L=0):
-        """L >= 1: decode continues a chunk-local recurrence of block L."""
+    def __init__(self, B, H, Dh, T_max, D, W=0, head_mask=None, device="cuda", L=0, kv_bits=16):
+        """L >= 1: decode continues a chunk-local recurrence of block L.
+
+        kv_bits: 16 holds the dilated rows in bf16; 4 holds them in 4 bits a
+        channel with a minimum and a step for every 32 channels (80 bytes a row
+        of 128 channels instead of 256); the last W positions and the state
+        stay bf16 and fp32.  Every method works on both."""
         lib = load_library()
+        if kv_bits not in (4, 16):
+            raise ValueError("kv_bits must be 4 or 16, got %r" % (kv_bits,))
+        self.kv_bits = int(kv_bits)
+        q4 = self.kv_bits == 4
+        size, init = ("ratp_cache_bytes_q4", "ratp_cache_init_q4") if q4 else ("ratp_cache_bytes", "ratp_cache_init")
         self.B, self.H, self.Dh, self.T_max, self.D, self.W = B, H, Dh, T_max, D, W
         self.head_mask = [1 if v else 0 for v in head_mask] if head_mask is not None else None
         self._mask_buf, mp = _mask_buf(self.head_mask, H)
         n = ctypes.c_size_t()
-        _check("ratp_cache_bytes", lib.ratp_cache_bytes(B, H, Dh, T_max, D, W, mp, ctypes.byref(n)))
+        _check(size, getattr(lib, size)(B, H, Dh, T_max, D, W, mp, ctypes.byref(n)))
         self.buffer = torch.empty(n.value, dtype=torch.uint8, device=device)
         self.c = CacheStruct()
-        _check("ratp_cache_init", lib.ratp_cache_init(
+        _check(init, getattr(lib, init)(
             ctypes.byref(self.c), _ptr(self.buffer), n.value, B, H, Dh, T_max, D, W, mp,
             _stream(self.buffer)))
         self.L = int(L)
@@ -445,7 +558,15 @@ class KVCache:
         return self.buffer[off: off + numel * esz].view(dtype)
 
     def dil_rows(self, which="k"):
-        """Kc or Vc as [B, rows_per_b, Dh] bf16 (a view of the buffer)."""
+        """Kc or Vc as [B, rows_per_b, Dh]: bf16, a view of the buffer; for a
+        4-bit cache the fp32 values that the held rows stand for."""
+        if self.kv_bits == 4:
+            out = torch.empty(self.B, self.c.rows_per_b, self.Dh, dtype=torch.float32, device=self.buffer.device)
+            with torch.cuda.device(out.device):
+                _check("ratp_cache_read_q4", load_library().ratp_cache_read_q4(
+                    ctypes.byref(self.c), _ptr(out) if which == "k" else None,
+                    None if which == "k" else _ptr(out), _stream(out)))
+            return out
         addr = self.c.Kc if which == "k" else self.c.Vc
         rows = self.B * self.c.rows_per_b
         return self._view(addr, rows * self.Dh, torch.bfloat16).view(self.B, self.c.rows_per_b, self.Dh)

@@ -75,6 +75,153 @@ __device__ __forceinline__ long long head_offset(const unsigned long long* bits,
   return (long long)nd * T_max + (long long)(h - nd) * (T_max / D);
 }
 
+// The head whose splits hold CTA `rem` of a batch item: last with split_base[h] <= rem.
+__device__ __forceinline__ int head_of_split(const Params& p, int rem) {
+  int lo = 0, hi = p.H - 1;
+  while (lo < hi) {
+    const int mid = (lo + hi + 1) >> 1;
+    if (p.split_base[mid] <= rem) lo = mid; else hi = mid - 1;
+  }
+  return lo;
+}
+
+// The recurrence step of (b, h) for both streams, by the CTA's kThreads
+// threads: new fp32 state, the bf16-rounded key/value into s_self_k /
+// s_self_v and the ring, and append(stream, channel, value) for each channel
+// (the caller's cached row).  Ends with a barrier.
+template <int DH, typename Append>
+__device__ __forceinline__ void recurrence_step(const Params& p, long long bh, int t, float* s_self_k, float* s_self_v,
+                                                Append append) {
+  const int tid = threadIdx.x;
+  [[maybe_unused]] const long long n_tok = (long long)p.B * p.H * DH;
+  [[maybe_unused]] const long long n_ring = (long long)p.B * p.H * p.W * DH;
+  const int WL = p.window_L;
+  [[maybe_unused]] const long long n_in = 3ll * p.B * p.H * (long long)WL * DH;    // input-ring elements
+  if (WL > 0) {
+    // this step's inputs into slot t mod WL; the window is then
+    // positions max(0, t - WL + 1) .. t of the ring
+    for (int c = tid; c < 3 * DH; c += kThreads) {
+      const int s3 = c / DH, ch = c % DH;
+      const __nv_bfloat16* src = (s3 == 0 ? p.xk : s3 == 1 ? p.xv : p.g) + bh * DH + ch;
+      const long long dst = (((long long)s3 * p.B * p.H + bh) * WL + t % WL) * DH + ch;
+      if (RATP_IN(dst, 1, n_in) && RATP_IN(bh * DH + ch, 1, n_tok)) p.in_ring[dst] = *src;
+    }
+    __syncthreads();
+  }
+  for (int c = tid; c < 2 * DH; c += kThreads) {
+    const int s = c / DH, ch = c % DH;
+    if (!RATP_IN(((long long)s * p.B * p.H + bh) * DH + ch, 1, 2 * n_tok) ||
+        !RATP_IN(bh * DH + ch, 1, n_tok)) continue;
+    float* st = p.state + ((long long)s * p.B * p.H + bh) * DH + ch;
+    const float x = __bfloat162float((s == 0 ? p.xk : p.xv)[bh * DH + ch]);
+    const float gg = __bfloat162float(p.g[bh * DH + ch]);
+    float hn;
+    if (WL > 0) {
+      // fixed look-back: the recurrence from zero over the window
+      const __nv_bfloat16* rx = p.in_ring + ((long long)s * p.B * p.H + bh) * WL * DH + ch;
+      const __nv_bfloat16* rg = p.in_ring + ((long long)2 * p.B * p.H + bh) * WL * DH + ch;
+      float acc_h = 0.f;
+      const int j0 = max(0, t - WL + 1);
+      if (!RATP_IN(((long long)2 * p.B * p.H + bh) * WL * DH, (long long)WL * DH, n_in)) continue;
+#pragma unroll 4
+      for (int j = j0; j <= t; ++j) {
+        const int slot = j % WL;
+        const float gj = __bfloat162float(rg[(long long)slot * DH]);
+        const float xj = __bfloat162float(rx[(long long)slot * DH]);
+        acc_h = fmaf(gj, acc_h - xj, xj);
+      }
+      hn = acc_h;
+    } else {
+      const float prev = (p.reset_L > 0 && t % p.reset_L == 0) ? 0.f : *st;
+      hn = fmaf(gg, prev - x, x);
+    }
+    *st = hn;
+    const __nv_bfloat16 hb = __float2bfloat16_rn(hn);
+    (s == 0 ? s_self_k : s_self_v)[ch] = __bfloat162float(hb);
+    append(s, ch, hb);
+    if (p.W > 0 && RATP_IN((bh * p.W + t % p.W) * DH + ch, 1, n_ring))
+      (s == 0 ? p.Kw : p.Vw)[(bh * p.W + t % p.W) * DH + ch] = hb;
+  }
+  __syncthreads();
+}
+
+// Merges the CTA's NG entries (running max s_m, sum s_l, accumulator s_acc; a
+// barrier precedes the call) and writes o, or this split's partial; the last
+// split of (b, h) to publish merges the partials.
+template <int DH, int NG>
+__device__ __forceinline__ void merge_entries(const Params& p, long long bh, int split, int n_used, const float* s_m,
+                                              const float* s_l, const float (*s_acc)[DH], int* s_last) {
+  const int tid = threadIdx.x;
+  [[maybe_unused]] const long long n_tok = (long long)p.B * p.H * DH;
+  float M = -INFINITY;
+#pragma unroll
+  for (int gi = 0; gi < NG; ++gi) M = fmaxf(M, s_m[gi]);
+  const bool single = (n_used == 1);
+  [[maybe_unused]] const long long n_part = (long long)p.B * p.H * p.max_splits * (DH + 2);
+  const bool part_ok = single || RATP_IN((bh * p.max_splits + split) * (DH + 2), DH + 2, n_part);
+  float* part = p.partial + (bh * p.max_splits + split) * (DH + 2);
+  for (int c = tid; c < DH; c += kThreads) {
+    float L = 0.f, A = 0.f;
+#pragma unroll
+    for (int gi = 0; gi < NG; ++gi) {
+      const float w = (s_m[gi] == -INFINITY) ? 0.f : exp2f(s_m[gi] - M);
+      L = fmaf(s_l[gi], w, L);
+      A = fmaf(s_acc[gi][c], w, A);
+    }
+    if (single) {
+      if (RATP_IN(bh * DH + c, 1, n_tok)) p.o[bh * DH + c] = __float2bfloat16_rn(A / L);
+    } else if (part_ok) {
+      __stcg(part + 2 + c, A);
+      if (c == 0) { __stcg(part, M); __stcg(part + 1, L); }
+    }
+  }
+  if (!single) {
+    __threadfence();
+    __syncthreads();
+    if (tid == 0) {
+      const unsigned int prev = atomicAdd(p.counters + bh, 1u);
+      *s_last = (prev == (unsigned int)(n_used - 1));
+    }
+    __syncthreads();
+    if (*s_last) {
+      __threadfence();
+      const float* pb = p.partial + bh * p.max_splits * (DH + 2);
+      const bool pb_ok = RATP_IN(bh * p.max_splits * (DH + 2), (long long)n_used * (DH + 2), n_part);
+      float MM = -INFINITY;
+      for (int i = 0; i < n_used; ++i) MM = fmaxf(MM, __ldcg(pb + i * (DH + 2)));
+      for (int c = tid; pb_ok && c < DH; c += kThreads) {
+        float L = 0.f, A = 0.f;
+        for (int i = 0; i < n_used; ++i) {
+          const float mi = __ldcg(pb + i * (DH + 2));
+          const float w = (mi == -INFINITY) ? 0.f : exp2f(mi - MM);
+          L = fmaf(__ldcg(pb + i * (DH + 2) + 1), w, L);
+          A = fmaf(__ldcg(pb + i * (DH + 2) + 2 + c), w, A);
+        }
+        if (RATP_IN(bh * DH + c, 1, n_tok)) p.o[bh * DH + c] = __float2bfloat16_rn(A / L);
+      }
+      if (tid == 0) p.counters[bh] = 0u;
+    }
+  }
+}
+
+// The last CTA of batch item b advances len[b] (one counter per batch item,
+// so the step's closing atomics spread over B addresses instead of one).
+__device__ __forceinline__ void advance_len(const Params& p, int b) {
+  __syncthreads();
+  if (threadIdx.x == 0) {
+    __threadfence();
+    uint32_t* cnt = p.counters + (long long)p.B * p.H + b;
+    const unsigned int prev = atomicAdd(cnt, 1u);
+    if (prev == (unsigned int)p.splits_per_b - 1u) {
+      __threadfence();
+      const int tb = p.len[b];
+      if (tb < p.T_max) p.len[b] = tb + 1;
+      *cnt = 0u;
+      __threadfence();
+    }
+  }
+}
+
 template <int DH>
 __global__ void __launch_bounds__(kThreads, 7)
 decode_kernel(const Params p) {
@@ -92,15 +239,7 @@ decode_kernel(const Params p) {
   // key count can need), then split
   const int b = blockIdx.x / p.splits_per_b;
   const int rem = blockIdx.x - b * p.splits_per_b;
-  int h = 0;
-  {
-    int lo = 0, hi = p.H - 1;                    // last head with split_base[h] <= rem
-    while (lo < hi) {
-      const int mid = (lo + hi + 1) >> 1;
-      if (p.split_base[mid] <= rem) lo = mid; else hi = mid - 1;
-    }
-    h = lo;
-  }
+  const int h = head_of_split(p, rem);
   const int split = rem - p.split_base[h];
   const int tid = threadIdx.x;
 
@@ -154,56 +293,13 @@ decode_kernel(const Params p) {
 
     // ---- split 0: recurrence step, append, ring write, self key ----
     if (split == 0) {
-      const int WL = p.window_L;
-      [[maybe_unused]] const long long n_in = 3ll * p.B * p.H * (long long)WL * DH;    // input-ring elements
-      if (WL > 0) {
-        // this step's inputs into slot t mod WL; the window is then
-        // positions max(0, t - WL + 1) .. t of the ring
-        for (int c = tid; c < 3 * DH; c += kThreads) {
-          const int s3 = c / DH, ch = c % DH;
-          const __nv_bfloat16* src = (s3 == 0 ? p.xk : s3 == 1 ? p.xv : p.g) + bh * DH + ch;
-          const long long dst = (((long long)s3 * p.B * p.H + bh) * WL + t % WL) * DH + ch;
-          if (RATP_IN(dst, 1, n_in) && RATP_IN(bh * DH + ch, 1, n_tok)) p.in_ring[dst] = *src;
-        }
-        __syncthreads();
-      }
-      for (int c = tid; c < 2 * DH; c += kThreads) {
-        const int s = c / DH, ch = c % DH;
-        if (!RATP_IN(((long long)s * p.B * p.H + bh) * DH + ch, 1, 2 * n_tok) ||
-            !RATP_IN(bh * DH + ch, 1, n_tok)) continue;
-        float* st = p.state + ((long long)s * p.B * p.H + bh) * DH + ch;
-        const float x = __bfloat162float((s == 0 ? p.xk : p.xv)[bh * DH + ch]);
-        const float gg = __bfloat162float(p.g[bh * DH + ch]);
-        float hn;
-        if (WL > 0) {
-          // fixed look-back: the recurrence from zero over the window
-          const __nv_bfloat16* rx = p.in_ring + ((long long)s * p.B * p.H + bh) * WL * DH + ch;
-          const __nv_bfloat16* rg = p.in_ring + ((long long)2 * p.B * p.H + bh) * WL * DH + ch;
-          float acc_h = 0.f;
-          const int j0 = max(0, t - WL + 1);
-          if (!RATP_IN(((long long)2 * p.B * p.H + bh) * WL * DH, (long long)WL * DH, n_in)) continue;
-#pragma unroll 4
-          for (int j = j0; j <= t; ++j) {
-            const int slot = j % WL;
-            const float gj = __bfloat162float(rg[(long long)slot * DH]);
-            const float xj = __bfloat162float(rx[(long long)slot * DH]);
-            acc_h = fmaf(gj, acc_h - xj, xj);
-          }
-          hn = acc_h;
-        } else {
-          const float prev = (p.reset_L > 0 && t % p.reset_L == 0) ? 0.f : *st;
-          hn = fmaf(gg, prev - x, x);
-        }
-        *st = hn;
-        const __nv_bfloat16 hb = __float2bfloat16_rn(hn);
-        (s == 0 ? s_self_k : s_self_v)[ch] = __bfloat162float(hb);
-        if (t % Dd == Dd - 1 && app_slot < p.T_max / Dd && RATP_IN((cache_row0 + app_slot) * DH + ch, 1, n_dil))
+      const bool keep = t % Dd == Dd - 1;
+      if (keep && app_slot >= p.T_max / Dd && tid == 0) raise_error(RATP_ERR_CAPACITY);
+      const bool room = keep && app_slot < p.T_max / Dd;
+      recurrence_step<DH>(p, bh, t, s_self_k, s_self_v, [&](int s, int ch, __nv_bfloat16 hb) {
+        if (room && RATP_IN((cache_row0 + app_slot) * DH + ch, 1, n_dil))
           (s == 0 ? p.Kc : p.Vc)[(cache_row0 + app_slot) * DH + ch] = hb;
-        if (p.W > 0 && RATP_IN((bh * p.W + t % p.W) * DH + ch, 1, n_ring))
-          (s == 0 ? p.Kw : p.Vw)[(bh * p.W + t % p.W) * DH + ch] = hb;
-      }
-      if (t % Dd == Dd - 1 && app_slot >= p.T_max / Dd && tid == 0) raise_error(RATP_ERR_CAPACITY);
-      __syncthreads();
+      });
     }
 
     // ---- stream this split's keys ----
@@ -305,73 +401,10 @@ decode_kernel(const Params p) {
 #pragma unroll
     for (int i = 0; i < 8; ++i) s_acc[grp][li * 8 + i] = acc[i];
     __syncthreads();
-    float M = -INFINITY;
-#pragma unroll
-    for (int gi = 0; gi < NG; ++gi) M = fmaxf(M, s_m[gi]);
-    const bool single = (n_used == 1);
-    [[maybe_unused]] const long long n_part = (long long)p.B * p.H * p.max_splits * (DH + 2);
-    const bool part_ok = single || RATP_IN((bh * p.max_splits + split) * (DH + 2), DH + 2, n_part);
-    float* part = p.partial + (bh * p.max_splits + split) * (DH + 2);
-    for (int c = tid; c < DH; c += kThreads) {
-      float L = 0.f, A = 0.f;
-#pragma unroll
-      for (int gi = 0; gi < NG; ++gi) {
-        const float w = (s_m[gi] == -INFINITY) ? 0.f : exp2f(s_m[gi] - M);
-        L = fmaf(s_l[gi], w, L);
-        A = fmaf(s_acc[gi][c], w, A);
-      }
-      if (single) {
-        if (RATP_IN(bh * DH + c, 1, n_tok)) p.o[bh * DH + c] = __float2bfloat16_rn(A / L);
-      } else if (part_ok) {
-        __stcg(part + 2 + c, A);
-        if (c == 0) { __stcg(part, M); __stcg(part + 1, L); }
-      }
-    }
-    if (!single) {
-      __threadfence();
-      __syncthreads();
-      if (tid == 0) {
-        const unsigned int prev = atomicAdd(p.counters + bh, 1u);
-        s_last = (prev == (unsigned int)(n_used - 1));
-      }
-      __syncthreads();
-      if (s_last) {
-        __threadfence();
-        const float* pb = p.partial + bh * p.max_splits * (DH + 2);
-        const bool pb_ok = RATP_IN(bh * p.max_splits * (DH + 2), (long long)n_used * (DH + 2), n_part);
-        float MM = -INFINITY;
-        for (int i = 0; i < n_used; ++i) MM = fmaxf(MM, __ldcg(pb + i * (DH + 2)));
-        for (int c = tid; pb_ok && c < DH; c += kThreads) {
-          float L = 0.f, A = 0.f;
-          for (int i = 0; i < n_used; ++i) {
-            const float mi = __ldcg(pb + i * (DH + 2));
-            const float w = (mi == -INFINITY) ? 0.f : exp2f(mi - MM);
-            L = fmaf(__ldcg(pb + i * (DH + 2) + 1), w, L);
-            A = fmaf(__ldcg(pb + i * (DH + 2) + 2 + c), w, A);
-          }
-          if (RATP_IN(bh * DH + c, 1, n_tok)) p.o[bh * DH + c] = __float2bfloat16_rn(A / L);
-        }
-        if (tid == 0) p.counters[bh] = 0u;
-      }
-    }
+    merge_entries<DH, NG>(p, bh, split, n_used, s_m, s_l, s_acc, &s_last);
   }
 
-  // ---- the last CTA of batch item b advances len[b] ----
-  // (one counter per batch item, so the step's closing atomics spread over
-  // B addresses instead of one)
-  __syncthreads();
-  if (tid == 0) {
-    __threadfence();
-    uint32_t* cnt = p.counters + (long long)p.B * p.H + b;
-    const unsigned int prev = atomicAdd(cnt, 1u);
-    if (prev == (unsigned int)p.splits_per_b - 1u) {
-      __threadfence();
-      const int tb = p.len[b];
-      if (tb < p.T_max) p.len[b] = tb + 1;
-      *cnt = 0u;
-      __threadfence();
-    }
-  }
+  advance_len(p, b);
 }
 
 // ---- prefill -> cache hand-off --------------------------------------------

@@ -6,7 +6,9 @@
 //   attn_tc.cuh    tensor-core (TMA + tcgen05) dilated/windowed attention
 //   attn_simt.cuh  CUDA-core attention for fp32 / head dim 64
 //   decode.cuh     cache pack and the fused decode step
+//   decode_q4.cuh  the same over a cache whose dilated rows are held in 4 bits
 //   window.cuh     fixed look-back recurrence (window of the last L tokens)
+//   norm_rope.cuh  RMS norm of q and k heads with the rotary position
 #include <cuda.h>
 #include <cuda_runtime.h>
 #include <string.h>
@@ -36,6 +38,8 @@ __global__ void guard_probe_kernel() {
 #include "attn_tc.cuh"
 #include "attn_simt.cuh"
 #include "decode.cuh"
+#include "decode_q4.cuh"
+#include "norm_rope.cuh"
 
 using namespace ratp;
 
@@ -489,45 +493,91 @@ int launch_prefill_fused(const void* q, const void* xk, const void* xv, const vo
   return launch_status();
 }
 
+// ---- q/k norm and rotary position ---------------------------------------------
+void fill_norm_rope(norm_rope::Tensor* a, const ratp_view* x, const ratp_view* y, const float* w, long long tokens) {
+  a->x = x->data; a->y = y->data; a->w = w;
+  a->xs_b = x->stride_b; a->xs_t = x->stride_t; a->xs_h = x->stride_h;
+  a->ys_b = y->stride_b; a->ys_t = y->stride_t; a->ys_h = y->stride_h;
+  a->H = x->heads;
+  // A token's heads stay in one group of lanes, which computes its sines once,
+  // unless the tokens alone cannot fill the GPU (kGroups groups of 16 lanes
+  // are resident); then they are split into blocks of whole unrolled steps.
+  const long long kGroups = (long long)sm_count() * 128;
+  const int steps = (x->heads + norm_rope::kUnroll - 1) / norm_rope::kUnroll;
+  long long want = tokens > 0 ? kGroups / (2 * tokens) : 1;
+  want = std::max(1ll, std::min(want, (long long)steps));
+  a->blk = (int)((steps + want - 1) / want) * norm_rope::kUnroll;
+  a->n_blk = (x->heads + a->blk - 1) / a->blk;
+}
+
+template <typename E>
+int launch_norm_rope(const norm_rope::Params& p, int Dh, cudaStream_t st) {
+  const int per = norm_rope::kThreads / (Dh / 8);
+  const long long grid = (p.units + per - 1) / per;
+  if (grid > 0x7fffffffll) return RATP_ERR_SHAPE;
+  if (Dh == 128) norm_rope::norm_rope_kernel<E, 128><<<(unsigned)grid, norm_rope::kThreads, 0, st>>>(p);
+  else norm_rope::norm_rope_kernel<E, 64><<<(unsigned)grid, norm_rope::kThreads, 0, st>>>(p);
+  return launch_status();
+}
+
+// a view of `heads` head rows: pointer, strides that keep rows 16-byte aligned
+int check_view(const ratp_view* v, int heads, int esize) {
+  if (v == nullptr || v->data == nullptr || v->heads != heads) return RATP_ERR_ARG;
+  if (v->stride_b < 0 || v->stride_t < 0 || v->stride_h < 0) return RATP_ERR_ARG;
+  if (!aligned16(v->data)) return RATP_ERR_ALIGN;
+  const long long q = 16 / esize;
+  if (v->stride_b % q || v->stride_t % q || v->stride_h % q) return RATP_ERR_ALIGN;
+  return RATP_OK;
+}
+
 // ---- cache ------------------------------------------------------------------
 struct CacheLayout {
   long long rows_per_b;
-  size_t off_kc, off_vc, off_kw, off_vw, off_len, off_part, off_cnt, total;
+  size_t off_kc, off_vc, off_kw, off_vw, off_len, off_part, off_cnt, off_kp, off_vp, total;
   int max_splits, split_keys;
 };
+
+// Keys of head (dense or not) as decode splits count them: a ring row of a
+// 4-bit cache counts as several 4-bit rows.
+long long split_units(bool dense, int T_max, int D, int W, int kv_bits) {
+  if (dense) return T_max;
+  return (long long)T_max / D + (long long)W * (kv_bits == 4 ? decode_q4::kRingUnits : 1);
+}
 
 // Decode grid sizing: keys per split chosen so that one step is about one
 // wave of CTAs (kDecodeCtasPerSm resident per SM), never below kMinSplitKeys.
 constexpr int kDecodeCtasPerSm = 6;
 constexpr int kMinSplitKeys = 128;
+constexpr int kDecodeCtasPerSmQ4 = 4;
+constexpr int kMinSplitKeysQ4 = 256;
 
 int cache_layout(int B, int H, int Dh, int T_max, int D, int W, const uint8_t* head_mask,
-                 CacheLayout* L) {
+                 int kv_bits, CacheLayout* L) {
   if (B < 1 || H < 1 || T_max < 1 || D < 1 || W < 0) return RATP_ERR_ARG;
   if (Dh != 128 && Dh != 64) return RATP_ERR_SHAPE;
   if (H > RATP_MAX_HEADS) return RATP_ERR_SHAPE;
-  long long per_b = 0, keys_total = 0;
-  int max_keys = 0;
+  const bool q4 = kv_bits == 4;
+  const long long min_split = q4 ? kMinSplitKeysQ4 : kMinSplitKeys;
+  long long per_b = 0, keys_total = 0, max_keys = 0;
   for (int h = 0; h < H; ++h) {
     const bool dense = head_mask != nullptr && head_mask[h] != 0;
-    const int cap = dense ? T_max : T_max / D;
-    per_b += cap;
-    const int keys = cap + (dense ? 0 : W);
+    per_b += dense ? T_max : T_max / D;
+    const long long keys = split_units(dense, T_max, D, W, kv_bits);
     keys_total += (long long)B * keys;
     if (keys > max_keys) max_keys = keys;
   }
   L->rows_per_b = per_b;
-  const long long target_ctas = (long long)sm_count() * kDecodeCtasPerSm;
+  const long long target_ctas = (long long)sm_count() * (q4 ? kDecodeCtasPerSmQ4 : kDecodeCtasPerSm);
   long long split = (keys_total + target_ctas - 1) / target_ctas;
-  if (split < kMinSplitKeys) split = kMinSplitKeys;
+  if (split < min_split) split = min_split;
   // Keep every head's split count but even out its splits: the split becomes
   // the largest per-split share among the heads, so no CTA streams more keys
   // than it must (7.6B hybrid: 357 -> 347 keys, 24 and 6 splits per head).
   {
-    long long even = kMinSplitKeys;
+    long long even = min_split;
     for (int h = 0; h < H; ++h) {
       const bool dense = head_mask != nullptr && head_mask[h] != 0;
-      const long long keys = (dense ? T_max : T_max / D) + (dense ? 0 : W);
+      const long long keys = split_units(dense, T_max, D, W, kv_bits);
       if (keys == 0) continue;
       const long long n = (keys + split - 1) / split;
       even = std::max(even, (keys + n - 1) / n);
@@ -536,19 +586,66 @@ int cache_layout(int B, int H, int Dh, int T_max, int D, int W, const uint8_t* h
   }
   if (split > (1 << 30)) split = 1 << 30;
   L->split_keys = (int)split;
-  L->max_splits = (max_keys + L->split_keys - 1) / L->split_keys;
+  L->max_splits = (int)((max_keys + L->split_keys - 1) / L->split_keys);
   if (L->max_splits < 1) L->max_splits = 1;
-  const size_t row_bytes = (size_t)Dh * 2;
+  const size_t ring_row = (size_t)Dh * 2, row_bytes = q4 ? (size_t)Dh / 2 : ring_row;
   size_t off = 0;
   auto take = [&](size_t bytes) { size_t o = off; off += scan::align256(bytes); return o; };
   L->off_kc = take((size_t)B * per_b * row_bytes);
   L->off_vc = take((size_t)B * per_b * row_bytes);
-  L->off_kw = take((size_t)B * H * W * row_bytes);
-  L->off_vw = take((size_t)B * H * W * row_bytes);
+  L->off_kw = take((size_t)B * H * W * ring_row);
+  L->off_vw = take((size_t)B * H * W * ring_row);
   L->off_len = take((size_t)B * 4);
   L->off_part = take((size_t)B * H * L->max_splits * (Dh + 2) * 4);
   L->off_cnt = take((size_t)(B * H + B) * 4);
+  const size_t par_bytes = q4 ? (size_t)B * per_b * (Dh / decode_q4::kGroup) * 4 : 0;
+  L->off_kp = take(par_bytes);
+  L->off_vp = take(par_bytes);
   L->total = off;
+  return RATP_OK;
+}
+
+int cache_bytes_common(int B, int H, int Dh, int T_max, int D, int W, const uint8_t* head_mask, int kv_bits,
+                       size_t* bytes) {
+  if (!bytes) return RATP_ERR_ARG;
+  CacheLayout L;
+  int rc = cache_layout(B, H, Dh, T_max, D, W, head_mask, kv_bits, &L);
+  if (rc) return rc;
+  *bytes = L.total;
+  return RATP_OK;
+}
+
+int cache_init_common(ratp_cache* c, void* buffer, size_t bytes, int B, int H, int Dh, int T_max,
+                      int D, int W, const uint8_t* head_mask, int kv_bits, void* stream) {
+  if (!c || !buffer) return RATP_ERR_ARG;
+  if (!aligned16(buffer)) return RATP_ERR_ALIGN;
+  CacheLayout L;
+  int rc = cache_layout(B, H, Dh, T_max, D, W, head_mask, kv_bits, &L);
+  if (rc) return rc;
+  if (bytes < L.total) return RATP_ERR_CAPACITY;
+  char* base = static_cast<char*>(buffer);
+  memset(c, 0, sizeof(*c));
+  c->Kc = base + L.off_kc;
+  c->Vc = base + L.off_vc;
+  c->Kw = W > 0 ? base + L.off_kw : nullptr;
+  c->Vw = W > 0 ? base + L.off_vw : nullptr;
+  c->len = reinterpret_cast<int32_t*>(base + L.off_len);
+  c->partial = reinterpret_cast<float*>(base + L.off_part);
+  c->counters = reinterpret_cast<uint32_t*>(base + L.off_cnt);
+  c->rows_per_b = L.rows_per_b;
+  c->B = B; c->H = H; c->Dh = Dh; c->T_max = T_max; c->D = D; c->W = W;
+  c->split_keys = L.split_keys;
+  c->max_splits = L.max_splits;
+  c->reset_L = 0;
+  c->window_L = 0;
+  c->in_ring = nullptr;
+  c->kv_bits = kv_bits;
+  c->Kp = kv_bits == 4 ? base + L.off_kp : nullptr;
+  c->Vp = kv_bits == 4 ? base + L.off_vp : nullptr;
+  for (int h = 0; h < H; ++h) c->dense[h] = (head_mask != nullptr && head_mask[h] != 0) ? 1 : 0;
+  cudaStream_t st = static_cast<cudaStream_t>(stream);
+  if (cudaMemsetAsync(c->len, 0, (size_t)B * 4, st) != cudaSuccess) return RATP_ERR_CUDA;
+  if (cudaMemsetAsync(c->counters, 0, (size_t)(B * H + B) * 4, st) != cudaSuccess) return RATP_ERR_CUDA;
   return RATP_OK;
 }
 
@@ -855,44 +952,87 @@ int ratp_dilated_attn_prefill_per_sample_ws(const void* q, const void* hk, const
                         static_cast<cudaStream_t>(stream));
 }
 
+int ratp_qk_norm_rope(const ratp_view* q, const ratp_view* k, const ratp_view* q_out, const ratp_view* k_out,
+                      const float* q_weight, const float* k_weight, const float* inv_freq,
+                      const int32_t* positions, int positions_per_token,
+                      int B, int T, int Dh, int rot, int interleaved, float eps, int dtype, void* stream) {
+  if (!q || !k || !q_out || !k_out || B < 0 || T < 0 || q->heads < 0 || k->heads < 0) return RATP_ERR_ARG;
+  if (dtype != RATP_F32 && dtype != RATP_BF16) return RATP_ERR_ARG;
+  if (!(eps >= 0.f && eps <= 3.0e38f)) return RATP_ERR_ARG;
+  if ((Dh != 64 && Dh != 128) || rot < 0 || rot > Dh || rot % 16 != 0) return RATP_ERR_SHAPE;
+  const int esize = dtype == RATP_BF16 ? 2 : 4;
+  const long long tokens = (long long)B * T;
+  if (tokens == 0 || (q->heads == 0 && k->heads == 0)) return RATP_OK;
+  if (rot > 0 && inv_freq == nullptr) return RATP_ERR_ARG;
+  const ratp_view* in[2] = {q, k};
+  const ratp_view* out[2] = {q_out, k_out};
+  const float* w[2] = {q_weight, k_weight};
+  norm_rope::Params p;
+  memset(&p, 0, sizeof(p));
+  p.inv_freq = inv_freq;
+  p.pos = positions;
+  p.pos_per_token = positions_per_token;
+  p.B = B; p.T = T; p.rot = rot; p.interleaved = interleaved;
+  p.eps = eps;
+  for (int i = 0; i < 2; ++i) {
+    if (in[i]->heads == 0) {
+      p.tensor[i].n_blk = 1;
+      p.tensor[i].blk = 0;
+      continue;
+    }
+    for (const ratp_view* v : {in[i], out[i]}) {
+      const int rc = check_view(v, in[i]->heads, esize);
+      if (rc) return rc;
+    }
+    if (w[i] != nullptr && !aligned16(w[i])) return RATP_ERR_ALIGN;
+    fill_norm_rope(&p.tensor[i], in[i], out[i], w[i], tokens);
+    const long long n = tokens * p.tensor[i].n_blk;
+    if (i == 0) p.units0 = n;
+    p.units += n;
+  }
+  if (!aligned16(inv_freq) || (reinterpret_cast<uintptr_t>(positions) & 3u) != 0) return RATP_ERR_ALIGN;
+  cudaStream_t st = static_cast<cudaStream_t>(stream);
+  return dtype == RATP_BF16 ? launch_norm_rope<__nv_bfloat16>(p, Dh, st) : launch_norm_rope<float>(p, Dh, st);
+}
+
 int ratp_cache_bytes(int B, int H, int Dh, int T_max, int D, int W,
                      const uint8_t* head_mask, size_t* bytes) {
-  if (!bytes) return RATP_ERR_ARG;
-  CacheLayout L;
-  int rc = cache_layout(B, H, Dh, T_max, D, W, head_mask, &L);
-  if (rc) return rc;
-  *bytes = L.total;
-  return RATP_OK;
+  return cache_bytes_common(B, H, Dh, T_max, D, W, head_mask, 16, bytes);
+}
+
+int ratp_cache_bytes_q4(int B, int H, int Dh, int T_max, int D, int W,
+                        const uint8_t* head_mask, size_t* bytes) {
+  return cache_bytes_common(B, H, Dh, T_max, D, W, head_mask, 4, bytes);
 }
 
 int ratp_cache_init(ratp_cache* c, void* buffer, size_t bytes, int B, int H, int Dh, int T_max,
                     int D, int W, const uint8_t* head_mask, void* stream) {
-  if (!c || !buffer) return RATP_ERR_ARG;
-  if (!aligned16(buffer)) return RATP_ERR_ALIGN;
-  CacheLayout L;
-  int rc = cache_layout(B, H, Dh, T_max, D, W, head_mask, &L);
-  if (rc) return rc;
-  if (bytes < L.total) return RATP_ERR_CAPACITY;
-  char* base = static_cast<char*>(buffer);
-  memset(c, 0, sizeof(*c));
-  c->Kc = base + L.off_kc;
-  c->Vc = base + L.off_vc;
-  c->Kw = W > 0 ? base + L.off_kw : nullptr;
-  c->Vw = W > 0 ? base + L.off_vw : nullptr;
-  c->len = reinterpret_cast<int32_t*>(base + L.off_len);
-  c->partial = reinterpret_cast<float*>(base + L.off_part);
-  c->counters = reinterpret_cast<uint32_t*>(base + L.off_cnt);
-  c->rows_per_b = L.rows_per_b;
-  c->B = B; c->H = H; c->Dh = Dh; c->T_max = T_max; c->D = D; c->W = W;
-  c->split_keys = L.split_keys;
-  c->max_splits = L.max_splits;
-  c->reset_L = 0;
-  c->window_L = 0;
-  c->in_ring = nullptr;
-  for (int h = 0; h < H; ++h) c->dense[h] = (head_mask != nullptr && head_mask[h] != 0) ? 1 : 0;
+  return cache_init_common(c, buffer, bytes, B, H, Dh, T_max, D, W, head_mask, 16, stream);
+}
+
+int ratp_cache_init_q4(ratp_cache* c, void* buffer, size_t bytes, int B, int H, int Dh, int T_max,
+                       int D, int W, const uint8_t* head_mask, void* stream) {
+  return cache_init_common(c, buffer, bytes, B, H, Dh, T_max, D, W, head_mask, 4, stream);
+}
+
+int ratp_cache_read_q4(const ratp_cache* c, float* k, float* v, void* stream) {
+  if (!c || c->kv_bits != 4) return RATP_ERR_ARG;
+  if ((k && !aligned16(k)) || (v && !aligned16(v))) return RATP_ERR_ALIGN;
+  const long long words = (long long)c->B * c->rows_per_b * (c->Dh / 8);
+  const long long grid = (words + 255) / 256;
+  if (grid == 0) return RATP_OK;
+  if (grid > 0x7fffffffll) return RATP_ERR_SHAPE;
   cudaStream_t st = static_cast<cudaStream_t>(stream);
-  if (cudaMemsetAsync(c->len, 0, (size_t)B * 4, st) != cudaSuccess) return RATP_ERR_CUDA;
-  if (cudaMemsetAsync(c->counters, 0, (size_t)(B * H + B) * 4, st) != cudaSuccess) return RATP_ERR_CUDA;
+  const void* codes[2] = {c->Kc, c->Vc};
+  const void* par[2] = {c->Kp, c->Vp};
+  float* out[2] = {k, v};
+  for (int i = 0; i < 2; ++i) {
+    if (out[i] == nullptr) continue;
+    decode_q4::unpack_kernel<<<(unsigned)grid, 256, 0, st>>>(static_cast<const uint32_t*>(codes[i]),
+                                                             static_cast<const uint32_t*>(par[i]), out[i], words);
+    const int rc = launch_status();
+    if (rc) return rc;
+  }
   return RATP_OK;
 }
 
@@ -922,8 +1062,18 @@ int ratp_cache_pack(ratp_cache* c, const void* hk, const void* hv, int T, void* 
   const int rpb = 256 / (c->Dh / 8);
   dim3 grid((unsigned)((max_rows + rpb - 1) / rpb), (unsigned)c->H, (unsigned)c->B);
   if (grid.x == 0) grid.x = 1;   // still sets len
-  if (c->Dh == 128) decode::pack_kernel<128><<<grid, 256, 0, st>>>(p);
-  else decode::pack_kernel<64><<<grid, 256, 0, st>>>(p);
+  if (c->kv_bits == 4) {
+    decode_q4::PackParams p4;
+    p4.d = p;
+    p4.Kp = static_cast<uint32_t*>(c->Kp);
+    p4.Vp = static_cast<uint32_t*>(c->Vp);
+    if (c->Dh == 128) decode_q4::pack_kernel<128><<<grid, 256, 0, st>>>(p4);
+    else decode_q4::pack_kernel<64><<<grid, 256, 0, st>>>(p4);
+  } else if (c->Dh == 128) {
+    decode::pack_kernel<128><<<grid, 256, 0, st>>>(p);
+  } else {
+    decode::pack_kernel<64><<<grid, 256, 0, st>>>(p);
+  }
   return launch_status();
 }
 
@@ -1023,7 +1173,7 @@ int decode_launch(const void* q, const void* xk, const void* xv, const void* g,
   p.split_base[0] = 0;
   for (int h = 0; h < c->H; ++h) {
     const bool dense = (p.dense_bits[h >> 6] >> (h & 63)) & 1ull;
-    const long long keys = dense ? (long long)c->T_max : (long long)c->T_max / c->D + c->W;
+    const long long keys = split_units(dense, c->T_max, c->D, c->W, c->kv_bits);
     long long sp = (keys + c->split_keys - 1) / c->split_keys;
     if (sp < 1) sp = 1;
     if (sp > c->max_splits) sp = c->max_splits;
@@ -1045,8 +1195,18 @@ int decode_launch(const void* q, const void* xk, const void* xv, const void* g,
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  cudaError_t e = (c->Dh == 128) ? cudaLaunchKernelEx(&cfg, decode::decode_kernel<128>, p)
-                                 : cudaLaunchKernelEx(&cfg, decode::decode_kernel<64>, p);
+  cudaError_t e;
+  if (c->kv_bits == 4) {
+    decode_q4::Params p4;
+    p4.d = p;
+    p4.Kp = static_cast<uint32_t*>(c->Kp);
+    p4.Vp = static_cast<uint32_t*>(c->Vp);
+    e = (c->Dh == 128) ? cudaLaunchKernelEx(&cfg, decode_q4::decode_kernel<128>, p4)
+                       : cudaLaunchKernelEx(&cfg, decode_q4::decode_kernel<64>, p4);
+  } else {
+    e = (c->Dh == 128) ? cudaLaunchKernelEx(&cfg, decode::decode_kernel<128>, p)
+                       : cudaLaunchKernelEx(&cfg, decode::decode_kernel<64>, p);
+  }
   if (e != cudaSuccess) return RATP_ERR_CUDA;
   return launch_status();
 }
