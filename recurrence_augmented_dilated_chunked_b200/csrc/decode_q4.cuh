@@ -37,12 +37,18 @@
 #include "common.cuh"
 #include "decode.cuh"
 
+#include <stddef.h>
+
 namespace ratp {
 namespace decode_q4 {
 
 constexpr int kThreads = 128;
 constexpr int kWarps = kThreads / 32;
-constexpr int kTile = 16;          // keys per warp step
+constexpr int kTile = 16;          // keys per MMA tile
+constexpr int kStep = 32;          // cached rows per warp step
+constexpr int kRingStep = 8;       // ring rows per warp step (their bytes fit the same stage)
+constexpr int kStages = 2;         // steps in flight per warp
+constexpr int kCtasPerSm = 4;
 constexpr int kGroup = 32;         // channels per scale
 // A ring key moves 512 bytes where a 4-bit key moves 160: it counts as three
 // when a (b, h)'s keys are split over CTAs.
@@ -50,51 +56,83 @@ constexpr int kRingUnits = 3;
 constexpr int kPrefetchRows = 128; // rows per split warmed into L2 before the wait
 
 struct Params {
-  decode::Params d;                // Kc / Vc hold codes (see codes())
+  decode::Params d;                // Kc / Vc hold code words, [B][rows_per_b][Dh / 8]
   uint32_t* Kp;                    // [B][rows_per_b][Dh / 32]
   uint32_t* Vp;
-};
-
-template <int DH>
-struct Row {
-  static constexpr int kWords = DH / 8;        // code words
-  static constexpr int kParams = DH / kGroup;  // parameter words
 };
 
 __device__ __forceinline__ float param_scale(uint32_t p) { return __uint_as_float(p << 16); }
 __device__ __forceinline__ float param_min(uint32_t p) { return __uint_as_float(p & 0xffff0000u); }
 
 // ---- quantisation -------------------------------------------------------------
-// IEEE division and rounding to nearest even throughout, so the codes are the
-// definition's.
+// Every step rounds as the definition does (to nearest even), so the codes are
+// the definition's.
 __device__ __forceinline__ uint32_t group_params(float lo, float hi) {
-  const __nv_bfloat16 s = __float2bfloat16_rn(__fdiv_rn(__fsub_rn(hi, lo), 15.f));
+  // d / 15 correctly rounded: the product's remainder is exact in one fma, and
+  // no quotient by 15 lies near enough to a rounding boundary to be missed
+  const float d = __fsub_rn(hi, lo), q = __fmul_rn(d, 1.f / 15.f);
+  const __nv_bfloat16 s = __float2bfloat16_rn(__fmaf_rn(__fmaf_rn(-15.f, q, d), 1.f / 15.f, q));
   const __nv_bfloat16 m = __float2bfloat16_rn(lo);   // exact: lo is a bf16 value
   return (uint32_t)__bfloat16_as_ushort(s) | ((uint32_t)__bfloat16_as_ushort(m) << 16);
 }
-__device__ __forceinline__ uint32_t code_of(float x, uint32_t par) {
-  const float s = param_scale(par);
-  if (!(s > 0.f)) return 0u;
-  const float n = rintf(__fdiv_rn(__fsub_rn(x, param_min(par)), s));
-  return (uint32_t)fminf(fmaxf(n, 0.f), 15.f);
+// rint(d / s) for d = x - m >= 0, as the integer added to 1.5 * 2^23 (its bits
+// hold it): the product with an approximate reciprocal is at most one off, and
+// the remainder d - n s, exact in one fma (n s has 12 bits), says where.  The
+// quotient's own rounding to fp32 never makes a tie: two fp32 numbers d whose
+// quotients by s straddle a tie lie further apart than half its last place.
+constexpr float kIntBias = 12582912.f;
+__device__ __forceinline__ uint32_t code_bits(float d, float s, float r) {
+  float nb = __fadd_rn(__fmul_rn(d, r), kIntBias);
+  const float n = nb - kIntBias;
+  const float rem = __fmaf_rn(-n, s, d);
+  const float twice = 2.f * fabsf(rem);
+  const bool off = twice > s || (twice == s && (__float_as_uint(nb) & 1u));
+  if (off) nb += copysignf(1.f, rem);
+  return __float_as_uint(nb);
 }
 __device__ __forceinline__ int nibble_shift(int c) { return 4 * ((c >> 1) + 4 * (c & 1)); }
 
-// 8 consecutive channels of a row -> one code word; the 4 lanes of a group of
-// 32 channels (consecutive, aligned) share its parameters.  All 4 call.
-__device__ __forceinline__ uint32_t quantise8(const float* f, uint32_t* par, unsigned lanes) {
-  float lo = f[0], hi = f[0];
+// 8 consecutive channels of a row (bf16 pairs) -> one code word; the 4 lanes of
+// a group of 32 channels (consecutive, aligned) share its parameters.  All 4
+// call.  A code is first taken from the quotient's product d r snapped to a
+// multiple of 2^-19 (2^-18 past 8) by the first addition, which makes exact
+// ties exact again, and rounded to even by the second; the remainder shows the
+// rare word in which a quotient that near a tie was none (x some 2^18 times
+// smaller than the group's minimum), and that word is done over.
+__device__ __forceinline__ uint32_t quantise8(const uint4& x, uint32_t* par, unsigned lanes) {
+  const uint32_t v[4] = {x.x, x.y, x.z, x.w};
+  __nv_bfloat162 lo2 = *reinterpret_cast<const __nv_bfloat162*>(&v[0]), hi2 = lo2;
 #pragma unroll
-  for (int i = 1; i < 8; ++i) { lo = fminf(lo, f[i]); hi = fmaxf(hi, f[i]); }
+  for (int i = 1; i < 4; ++i) {
+    const __nv_bfloat162 e = *reinterpret_cast<const __nv_bfloat162*>(&v[i]);
+    lo2 = __hmin2(lo2, e);
+    hi2 = __hmax2(hi2, e);
+  }
+  float lo = fminf(__low2float(lo2), __high2float(lo2)), hi = fmaxf(__low2float(hi2), __high2float(hi2));
 #pragma unroll
   for (int off = 1; off < 4; off <<= 1) {
     lo = fminf(lo, __shfl_xor_sync(lanes, lo, off));
     hi = fmaxf(hi, __shfl_xor_sync(lanes, hi, off));
   }
   *par = group_params(lo, hi);
+  const float s = param_scale(*par), m = param_min(*par);
+  if (!(s > 0.f)) return 0u;                   // a constant group
+  const float r0 = __fdividef(1.f, s), r = __fmaf_rn(r0, __fmaf_rn(-s, r0, 1.f), r0);   // 1 / s within 2^-24
+  float f[8];
+  Elem<__nv_bfloat16>::unpack(x, f);
   uint32_t w = 0;
+  float far = 0.f;
 #pragma unroll
-  for (int i = 0; i < 8; ++i) w |= code_of(f[i], *par) << nibble_shift(i);
+  for (int i = 0; i < 8; ++i) {
+    const float d = __fsub_rn(f[i], m);
+    const float nb = __fadd_rn(__fmaf_rn(d, r, 24.f), kIntBias - 24.f);
+    far = fmaxf(far, fabsf(__fmaf_rn(kIntBias - nb, s, d)));
+    w += (__float_as_uint(nb) - 0x4b400000u) << nibble_shift(i);
+  }
+  if (2.f * far <= s) return w;
+  w = 0;
+#pragma unroll
+  for (int i = 0; i < 8; ++i) w |= (code_bits(__fsub_rn(f[i], m), s, r) & 15u) << nibble_shift(i);
   return w;
 }
 
@@ -103,66 +141,106 @@ struct PackParams {
   decode::PackParams d;
   uint32_t* Kp;
   uint32_t* Vp;
+  int base[RATP_MAX_HEADS + 1];    // first block (within a batch item) of each head
 };
 
-// The grid and row numbering of decode::pack_kernel: Dh/8 threads per row,
-// dilated rows first (quantised), then the ring rows (copied).
+// The last head h < H with base[h] <= at.
+__device__ __forceinline__ int head_at(const int* base, int H, int at) {
+  int lo = 0, hi = H - 1;
+  while (lo < hi) {
+    const int mid = (lo + hi + 1) >> 1;
+    if (base[mid] <= at) lo = mid; else hi = mid - 1;
+  }
+  return lo;
+}
+
+// Dh/8 threads per row, kPackRows rows per thread; a block holds rows of one
+// (b, h): its dilated rows first (quantised), then its ring rows (copied).
+// Heads take blocks as they need (base[h]): a dense head has D times a dilated
+// one's rows.  A thread has all its rows' loads in flight at once, and the
+// block's index arithmetic is spread over them.
+constexpr int kPackRows = 4;
 template <int DH>
 __global__ void __launch_bounds__(256)
 pack_kernel(const PackParams pp) {
   const decode::PackParams& p = pp.d;
   constexpr int TPR = DH / 8;
   constexpr int RPB = 256 / TPR;
-  const int h = blockIdx.y, b = blockIdx.z;
-  const int r = blockIdx.x * RPB + threadIdx.x / TPR;
+  const int b = blockIdx.x / pp.base[p.H], at = blockIdx.x - b * pp.base[p.H];
+  const int h = head_at(pp.base, p.H, at);
+  const int r0 = (at - pp.base[h]) * (RPB * kPackRows) + threadIdx.x / TPR;
   const int li = threadIdx.x % TPR;
   const bool dense = decode::is_dense(p.dense_bits, h);
   const int Dd = dense ? 1 : p.D;
   const int n_dil = p.T / Dd;
   const int w_lo = max(0, p.T - p.W);
   const int n_ring = (p.W > 0) ? (p.T - w_lo) : 0;
-  if (blockIdx.x == 0 && h == 0 && threadIdx.x == 0) p.len[b] = p.T;
+  if (at == 0 && threadIdx.x == 0) p.len[b] = p.T;
   const long long src_base = (long long)b * p.T * p.H * DH + (long long)h * DH + li * 8;
   [[maybe_unused]] const long long n_src = (long long)p.B * p.T * p.H * DH;
+  const long long row0 = (long long)b * p.rows_per_b + decode::head_offset(p.dense_bits, h, p.T_max, p.D);
   const unsigned lanes = 0xfu << ((threadIdx.x & 31) & ~3);
-  if (r < n_dil) {
-    const long long src = src_base + ((long long)r * Dd + Dd - 1) * p.H * DH;
-    const long long row = (long long)b * p.rows_per_b + decode::head_offset(p.dense_bits, h, p.T_max, p.D) + r;
-    if (!RATP_IN(src, 8, n_src) || !RATP_IN(row, 1, (long long)p.B * p.rows_per_b)) return;
+
+  uint4 in[kPackRows][2];
 #pragma unroll
-    for (int s = 0; s < 2; ++s) {
-      float f[8];
-      uint32_t par;
-      Elem<__nv_bfloat16>::unpack(__ldcs(reinterpret_cast<const uint4*>((s == 0 ? p.hk : p.hv) + src)), f);
-      const uint32_t w = quantise8(f, &par, lanes);
-      reinterpret_cast<uint32_t*>(s == 0 ? p.Kc : p.Vc)[row * (DH / 8) + li] = w;
-      if ((li & 3) == 0) (s == 0 ? pp.Kp : pp.Vp)[row * (DH / kGroup) + li / 4] = par;
-    }
-  } else if (r < n_dil + n_ring) {
-    const int pos = w_lo + (r - n_dil);
+  for (int i = 0; i < kPackRows; ++i) {
+    const int r = r0 + i * RPB;
+    const int pos = r < n_dil ? r * Dd + Dd - 1 : w_lo + (r - n_dil);
     const long long src = src_base + (long long)pos * p.H * DH;
-    const long long dst = (((long long)b * p.H + h) * p.W + pos % p.W) * DH + li * 8;
-    if (!RATP_IN(src, 8, n_src) || !RATP_IN(dst, 8, (long long)p.B * p.H * p.W * DH)) return;
-    *reinterpret_cast<uint4*>(p.Kw + dst) = *reinterpret_cast<const uint4*>(p.hk + src);
-    *reinterpret_cast<uint4*>(p.Vw + dst) = *reinterpret_cast<const uint4*>(p.hv + src);
+    in[i][0] = in[i][1] = make_uint4(0u, 0u, 0u, 0u);
+    if (r < n_dil + n_ring && RATP_IN(src, 8, n_src)) {
+      in[i][0] = __ldcs(reinterpret_cast<const uint4*>(p.hk + src));
+      in[i][1] = __ldcs(reinterpret_cast<const uint4*>(p.hv + src));
+    }
+  }
+#pragma unroll
+  for (int i = 0; i < kPackRows; ++i) {
+    const int r = r0 + i * RPB;                // the same for a group's 4 lanes
+    if (r < n_dil) {
+      const long long row = row0 + r;
+      if (!RATP_IN(row, 1, (long long)p.B * p.rows_per_b)) continue;
+#pragma unroll
+      for (int s = 0; s < 2; ++s) {
+        uint32_t par;
+        const uint32_t w = quantise8(in[i][s], &par, lanes);
+        reinterpret_cast<uint32_t*>(s == 0 ? p.Kc : p.Vc)[row * (DH / 8) + li] = w;
+        if ((li & 3) == 0) (s == 0 ? pp.Kp : pp.Vp)[row * (DH / kGroup) + li / 4] = par;
+      }
+    } else if (r < n_dil + n_ring) {
+      const long long dst = (((long long)b * p.H + h) * p.W + (w_lo + (r - n_dil)) % p.W) * DH + li * 8;
+      if (!RATP_IN(dst, 8, (long long)p.B * p.H * p.W * DH)) continue;
+      *reinterpret_cast<uint4*>(p.Kw + dst) = in[i][0];
+      *reinterpret_cast<uint4*>(p.Vw + dst) = in[i][1];
+    }
   }
 }
 
 // ---- read-back: the values that the held rows stand for, fp32 ------------------
-// One thread per code word (8 channels): out[row][8 w .. 8 w + 7].
+// A thread takes kReadPer quads of 4 channels, a block's width apart, so that
+// every store of a warp is 512 contiguous bytes.
+constexpr int kReadPer = 4;
 __global__ void __launch_bounds__(256)
 unpack_kernel(const uint32_t* __restrict__ codes, const uint32_t* __restrict__ params, float* __restrict__ out,
-              long long words) {
-  const long long i = (long long)blockIdx.x * 256 + threadIdx.x;
-  if (i >= words) return;
-  const uint32_t w = __ldcs(codes + i), par = params[i >> 2];
-  const float s = param_scale(par), m = param_min(par);
-  float f[8];
+              long long quads) {
+  const long long i0 = (long long)blockIdx.x * (256 * kReadPer) + threadIdx.x;
+  uint32_t w[kReadPer], par[kReadPer];
 #pragma unroll
-  for (int c = 0; c < 8; ++c) f[c] = __fadd_rn(m, __fmul_rn((float)((w >> nibble_shift(c)) & 15u), s));
-  float4* o = reinterpret_cast<float4*>(out) + 2 * i;
-  __stcs(o, make_float4(f[0], f[1], f[2], f[3]));
-  __stcs(o + 1, make_float4(f[4], f[5], f[6], f[7]));
+  for (int j = 0; j < kReadPer; ++j) {
+    const long long i = i0 + 256 * j;
+    w[j] = i < quads ? codes[i >> 1] : 0u;
+    par[j] = i < quads ? params[i >> 3] : 0u;
+  }
+#pragma unroll
+  for (int j = 0; j < kReadPer; ++j) {
+    const long long i = i0 + 256 * j;
+    if (i >= quads) return;
+    const float s = param_scale(par[j]), m = param_min(par[j]);
+    const uint32_t x = w[j] >> ((i & 1) * 8);  // channels 4, 5, 6, 7 are the nibbles 2, 6, 3, 7
+    float f[4];
+#pragma unroll
+    for (int c = 0; c < 4; ++c) f[c] = __fadd_rn(m, __fmul_rn((float)((x >> nibble_shift(c)) & 15u), s));
+    __stcs(reinterpret_cast<float4*>(out) + i, make_float4(f[0], f[1], f[2], f[3]));
+  }
 }
 
 // ---- decode -------------------------------------------------------------------
@@ -175,221 +253,304 @@ __device__ __forceinline__ void mma_bf16(float* c, uint32_t a0, uint32_t a1, uin
 }
 
 // Code pairs of a word as bf16 pairs 128 + n (channels 2i, 2i + 1).
-__device__ __forceinline__ uint32_t pair_of(uint32_t w, int i) { return ((w >> (4 * i)) & 0x000f000fu) | 0x43004300u; }
+__device__ __forceinline__ uint32_t pair_of(uint32_t w, int i) {
+  uint32_t r;
+  asm("lop3.b32 %0, %1, %2, %3, 0xea;" : "=r"(r) : "r"(w >> (4 * i)), "r"(0x000f000fu), "r"(0x43004300u));   // (a & b) | c
+  return r;
+}
 
-// One tile of up to 16 keys as a warp holds it: lane (g, t) has the K words of
-// keys g, g + 8 (its channel quarter) and the V words of keys t, 4 + t, 8 + t,
-// 12 + t (channels [g Dh/8, (g + 1) Dh/8)), with the parameters it needs.
 template <int DH>
-struct Tile4 {
-  static constexpr int NW = DH / 64 * 2;       // K words per key and lane (16 or 32 channels)
-  static constexpr int NV = DH / 64;           // V words per key and lane (8 or 16 channels)
-  uint32_t k[2][NW];
-  uint32_t kp[2][2];                           // lanes t < 2: quarters 2t, 2t + 1
-  uint32_t v[4][NV];
-  uint32_t vp[4];                              // quarter g % 4
+struct Lane {
+  static constexpr int NW = DH / 32;           // K words per key and lane (a quarter of the channels)
+  static constexpr int NV = DH / 64;           // V words per key and lane (an eighth)
+};
+
+// A warp's stage in shared memory: kStep keys' codes and parameters of K and V.
+template <int DH>
+struct Stage {
+  uint32_t k[kStep][DH / 8];
+  uint32_t v[kStep][DH / 8];
+  uint32_t kp[kStep][DH / kGroup];
+  uint32_t vp[kStep][DH / kGroup];
+};
+
+// Copies BYTES to shared memory; with there == false, zeros.
+template <int BYTES>
+__device__ __forceinline__ void cp_async(uint32_t dst, const void* src, bool there) {
+  const int n = there ? BYTES : 0;
+  if constexpr (BYTES == 16)
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" :: "r"(dst), "l"(src), "r"(n) : "memory");
+  else
+    asm volatile("cp.async.ca.shared.global [%0], [%1], 8, %2;" :: "r"(dst), "l"(src), "r"(n) : "memory");
+}
+
+// Copies kStep rows of W words, BYTES at a time over the warp's lanes: src and
+// dst are this lane's first chunk.  Rows from n on are not read but zeroed.
+template <int W, int BYTES>
+__device__ __forceinline__ void copy_rows(uint32_t dst, const uint32_t* src, int n, int lane) {
+  constexpr int kPer = kStep * W * 4 / (32 * BYTES);   // chunks per lane
+  static_assert(kStep * W * 4 % (32 * BYTES) == 0, "whole warps of chunks");
+  if (n == kStep) {
+#pragma unroll
+    for (int i = 0; i < kPer; ++i) cp_async<BYTES>(dst + i * 32 * BYTES, src + i * 8 * BYTES, true);
+  } else {
+#pragma unroll
+    for (int i = 0; i < kPer; ++i) {
+      const bool there = (i * 32 + lane) * BYTES / (W * 4) < n;
+      cp_async<BYTES>(dst + i * 32 * BYTES, there ? src + i * 8 * BYTES : src - lane * (BYTES / 4), there);
+    }
+  }
+}
+
+// A warp's walk over its cached rows: this lane's first chunk of each array.
+template <int DH>
+struct Walk {
+  static constexpr int W = DH / 8, P = DH / kGroup;
+  static constexpr int kParBytes = P == 4 ? 16 : 8;    // a parameter row of 8 bytes is only 8-byte aligned
+  const uint32_t *k, *kp, *v, *vp;
+  __device__ __forceinline__ void start(const uint32_t* kc, const uint32_t* kpar, const uint32_t* vc,
+                                        const uint32_t* vpar, long long row, int lane) {
+    k = kc + row * W + lane * 4;
+    v = vc + row * W + lane * 4;
+    kp = kpar + row * P + lane * (kParBytes / 4);
+    vp = vpar + row * P + lane * (kParBytes / 4);
+  }
+  __device__ __forceinline__ void fetch(uint32_t stage, int n, int lane) const {
+    using S = Stage<DH>;
+    copy_rows<W, 16>(stage + (uint32_t)offsetof(S, k) + lane * 16, k, n, lane);
+    copy_rows<P, kParBytes>(stage + (uint32_t)offsetof(S, kp) + lane * kParBytes, kp, n, lane);
+    copy_rows<W, 16>(stage + (uint32_t)offsetof(S, v) + lane * 16, v, n, lane);
+    copy_rows<P, kParBytes>(stage + (uint32_t)offsetof(S, vp) + lane * kParBytes, vp, n, lane);
+  }
+  __device__ __forceinline__ void advance(int rows) {
+    k += rows * W; v += rows * W;
+    kp += rows * P; vp += rows * P;
+  }
 };
 
 template <int N>
-__device__ __forceinline__ void load_words(uint32_t* r, const uint32_t* src) {
+__device__ __forceinline__ void read_words(uint32_t* r, const uint32_t* src) {
   if constexpr (N == 4) {
-    const uint4 x = __ldcs(reinterpret_cast<const uint4*>(src));
+    const uint4 x = *reinterpret_cast<const uint4*>(src);
     r[0] = x.x; r[1] = x.y; r[2] = x.z; r[3] = x.w;
   } else if constexpr (N == 2) {
-    const uint2 x = __ldcs(reinterpret_cast<const uint2*>(src));
+    const uint2 x = *reinterpret_cast<const uint2*>(src);
     r[0] = x.x; r[1] = x.y;
   } else {
-    r[0] = __ldcs(src);
+    r[0] = *src;
   }
 }
 
-template <int DH>
-__device__ __forceinline__ void load_tile(Tile4<DH>& f, const uint32_t* kc, const uint32_t* kp, const uint32_t* vc,
-                                          const uint32_t* vp, int n, int g, int t) {
-  constexpr int W = DH / 8, P = DH / kGroup;
-  constexpr int NW = Tile4<DH>::NW, NV = Tile4<DH>::NV;
-#pragma unroll
-  for (int r = 0; r < 2; ++r) {
-    const int key = g + 8 * r;
-#pragma unroll
-    for (int i = 0; i < NW; ++i) f.k[r][i] = 0;
-    f.kp[r][0] = f.kp[r][1] = 0;
-    if (key < n) {
-      load_words<NW>(f.k[r], kc + key * W + t * NW);
-      if (t < 2) {
-        if constexpr (P == 4) load_words<2>(f.kp[r], kp + key * P + 2 * t);
-        else f.kp[r][0] = f.kp[r][1] = __ldcs(kp + key * P + t);
-      }
-    }
-  }
-#pragma unroll
-  for (int j = 0; j < 4; ++j) {
-    const int key = 4 * j + t;
-#pragma unroll
-    for (int i = 0; i < NV; ++i) f.v[j][i] = 0;
-    f.vp[j] = 0;
-    if (key < n) {
-      load_words<NV>(f.v[j], vc + key * W + g * NV);
-      f.vp[j] = __ldcs(vp + key * P + (g & 3) * P / 4);
-    }
-  }
-}
-
-// Running softmax of one warp: m, l (this lane's share) and the accumulators.
+// Running softmax of one warp.  m is the reference of the weights 2^(s - m):
+// it follows the running maximum only when a score passes it by more than
+// kSlack, so a weight is at most 2^kSlack and most steps rescale nothing.
+constexpr float kSlack = 8.f;
 template <int DH>
 struct Acc {
-  float m, l;
-  float z;                 // this lane's column: fp32 share of the minima and offsets
+  float m, l;              // l: this lane's share
+  float zm, zo;            // this lane's column: fp32 sums of w m and of the offset's share
   float c[DH / 16][4];     // MMA j: channels 2 of this lane's Dh/8 x columns
 };
 
-// Scores of the tile's keys g, g + 8 (log2 units; -inf past n) into the
-// softmax: rescales on a new maximum, returns the weights.
-template <int DH>
-__device__ __forceinline__ void weigh(Acc<DH>& a, float s0, float s1, int n, int g, float* p0, float* p1) {
-  s0 = g < n ? s0 : -INFINITY;
-  s1 = g + 8 < n ? s1 : -INFINITY;
-  float m = fmaxf(s0, s1);
+template <int DH, int N>
+__device__ __forceinline__ void weigh(Acc<DH>& a, const float* s, float* p) {
+  float top = s[0];
 #pragma unroll
-  for (int off = 4; off < 32; off <<= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, off));
-  m = fmaxf(m, a.m);
-  if (m > a.m) {           // the whole warp agrees
+  for (int i = 1; i < N; ++i) top = fmaxf(top, s[i]);
+  if (__any_sync(0xffffffffu, top > a.m + kSlack)) {       // always so at the first finite score (m = -inf)
+#pragma unroll
+    for (int off = 4; off < 32; off <<= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, off));
+    const float m = fmaxf(a.m, top);
     const float r = exp2f(a.m - m);
     a.l *= r;
-    a.z *= r;
+    a.zm *= r;
+    a.zo *= r;
 #pragma unroll
     for (int j = 0; j < DH / 16; ++j)
 #pragma unroll
       for (int i = 0; i < 4; ++i) a.c[j][i] *= r;
     a.m = m;
   }
-  *p0 = m == -INFINITY ? 0.f : exp2f(s0 - m);
-  *p1 = m == -INFINITY ? 0.f : exp2f(s1 - m);
-  a.l += *p0 + *p1;
+  const float m = a.m == -INFINITY ? 0.f : a.m;
+#pragma unroll
+  for (int i = 0; i < N; ++i) {
+    p[i] = exp2f(s[i] - m);
+    a.l += p[i];
+  }
 }
 
-// Weights of this lane's column for keys t, 4 + t, 8 + t, 12 + t: column < 4
-// the bf16 part, column >= 4 the bf16 rest of w.
-__device__ __forceinline__ float part_of(float w, int g) {
-  const float hi = __bfloat162float(__float2bfloat16_rn(w));
-  return g < 4 ? hi : __bfloat162float(__float2bfloat16_rn(w - hi));
+// B operand of the values: this lane's column of the weights x[0..3] of keys
+// t, 4 + t, 8 + t, 12 + t.  rest = 0 (columns 0..3): their bf16 parts; rest =
+// 1 (columns 4..7): the bf16 of what those leave.  sum: what was taken.
+__device__ __forceinline__ void split_weights(const float* x, float rest, uint32_t* b, float* sum) {
+  float got = 0.f;
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+    const uint32_t hi = pack_bf16x2(x[2 * i], x[2 * i + 1]);
+    const float y0 = fmaf(-rest, __uint_as_float(hi << 16), x[2 * i]);
+    const float y1 = fmaf(-rest, __uint_as_float(hi & 0xffff0000u), x[2 * i + 1]);
+    b[i] = pack_bf16x2(y0, y1);
+    got += __uint_as_float(b[i] << 16) + __uint_as_float(b[i] & 0xffff0000u);
+  }
+  *sum = got;
+}
+
+// Weights of keys t, 4 + t, 8 + t, 12 + t of a 16-key tile, whose lane (g, t)
+// holds those of keys g (p0) and g + 8 (p1).
+__device__ __forceinline__ void gather_weights(float p0, float p1, int t, float* pw) {
+  pw[0] = __shfl_sync(0xffffffffu, p0, 4 * t);
+  pw[1] = __shfl_sync(0xffffffffu, p0, 16 + 4 * t);
+  pw[2] = __shfl_sync(0xffffffffu, p1, 4 * t);
+  pw[3] = __shfl_sync(0xffffffffu, p1, 16 + 4 * t);
 }
 
 template <int DH>
-__device__ __forceinline__ void attend_codes(Acc<DH>& a, const Tile4<DH>& f, const uint32_t (*qf)[2], const float* qsum,
-                                             float scale_log2, int n, int g, int t) {
-  constexpr int NW = Tile4<DH>::NW, NV = Tile4<DH>::NV;
-  float d[4] = {0.f, 0.f, 0.f, 0.f};
+__device__ __forceinline__ void attend_codes(Acc<DH>& a, const Stage<DH>& st, const uint32_t (*qf)[2],
+                                             const float* qsum, float scale_log2, int n, int g, int t) {
+  constexpr int NW = Lane<DH>::NW, NV = Lane<DH>::NV, P = DH / kGroup;
+  constexpr int R = kStep / 8;                 // keys g + 8 r of this lane
+  float s[R], p[R];
 #pragma unroll
-  for (int j = 0; j < 2 * NW; ++j) {           // 4 channels of each quarter per MMA
-    const int w = j / 2, i = 2 * (j % 2);
-    mma_bf16(d, pair_of(f.k[0][w], i), pair_of(f.k[1][w], i), pair_of(f.k[0][w], i + 1), pair_of(f.k[1][w], i + 1),
-             qf[j][0], qf[j][1]);
+  for (int u = 0; u < kStep / kTile; ++u) {
+    uint32_t w0[NW], w1[NW];
+    read_words<NW>(w0, &st.k[16 * u + g][t * NW]);
+    read_words<NW>(w1, &st.k[16 * u + g + 8][t * NW]);
+    float d[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+    for (int j = 0; j < 2 * NW; ++j) {         // 4 channels of each quarter per MMA
+      const int w = j / 2, i = 2 * (j % 2);
+      mma_bf16(d, pair_of(w0[w], i), pair_of(w1[w], i), pair_of(w0[w], i + 1), pair_of(w1[w], i + 1), qf[j][0], qf[j][1]);
+    }
+    // lanes t = 0, 1 hold quarters (0, 1) and (2, 3); the others' columns are
+    // zero, and so are their qsum
+#pragma unroll
+    for (int r = 0; r < 2; ++r) {
+      uint32_t par[2];
+      if constexpr (P == 4) read_words<2>(par, &st.kp[16 * u + g + 8 * r][2 * (t & 1)]);
+      else par[0] = par[1] = st.kp[16 * u + g + 8 * r][t & 1];
+      const float sa = param_scale(par[0]), sb = param_scale(par[1]);
+      float x = fmaf(sa, fmaf(-128.f, qsum[0], d[2 * r]), param_min(par[0]) * qsum[0]);
+      x += fmaf(sb, fmaf(-128.f, qsum[1], d[2 * r + 1]), param_min(par[1]) * qsum[1]);
+      x += __shfl_xor_sync(0xffffffffu, x, 1);
+      s[2 * u + r] = __shfl_sync(0xffffffffu, x, 0, 4) * scale_log2;
+    }
   }
-  // lanes t = 0, 1 hold quarters (0, 1) and (2, 3); the others' columns are unused
-  float s[2];
+  if (n < kStep) {
 #pragma unroll
-  for (int r = 0; r < 2; ++r) {
-    const float sa = param_scale(f.kp[r][0]), sb = param_scale(f.kp[r][1]);
-    float x = fmaf(sa, d[2 * r], fmaf(sb, d[2 * r + 1], 0.f));
-    x = fmaf(fmaf(-128.f, sa, param_min(f.kp[r][0])), qsum[0], x);
-    x = fmaf(fmaf(-128.f, sb, param_min(f.kp[r][1])), qsum[1], x);
-    x += __shfl_xor_sync(0xffffffffu, x, 1);
-    s[r] = __shfl_sync(0xffffffffu, x, 0, 4) * scale_log2;
+    for (int r = 0; r < R; ++r)
+      if (8 * r + g >= n) s[r] = -INFINITY;
   }
-  float p0, p1;
-  weigh(a, s[0], s[1], n, g, &p0, &p1);
-  // this lane's column weights for keys t, 4 + t, 8 + t, 12 + t
-  float pw[4] = {__shfl_sync(0xffffffffu, p0, 4 * t), __shfl_sync(0xffffffffu, p0, 16 + 4 * t),
-                 __shfl_sync(0xffffffffu, p1, 4 * t), __shfl_sync(0xffffffffu, p1, 16 + 4 * t)};
-  float x[4];
+  weigh<DH, R>(a, s, p);
+  const float rest = g < 4 ? 0.f : 1.f;
 #pragma unroll
-  for (int j = 0; j < 4; ++j) {
-    x[j] = part_of(pw[j] * param_scale(f.vp[j]), g);
-    a.z = fmaf(-128.f, x[j], a.z);
-    if (g < 4) a.z = fmaf(pw[j], param_min(f.vp[j]), a.z);
-  }
-  const uint32_t b0 = pack_bf16x2(x[0], x[1]), b1 = pack_bf16x2(x[2], x[3]);
+  for (int u = 0; u < kStep / kTile; ++u) {
+    float pw[4], x[4], got;
+    gather_weights(p[2 * u], p[2 * u + 1], t, pw);
 #pragma unroll
-  for (int w = 0; w < NV; ++w) {
-    // low halves: channels 0, 2, 4, 6 of the word; high halves: 1, 3, 5, 7
-    const uint32_t l01 = __byte_perm(f.v[0][w], f.v[1][w], 0x5410), h01 = __byte_perm(f.v[0][w], f.v[1][w], 0x7632);
-    const uint32_t l23 = __byte_perm(f.v[2][w], f.v[3][w], 0x5410), h23 = __byte_perm(f.v[2][w], f.v[3][w], 0x7632);
+    for (int j = 0; j < 4; ++j) {
+      const uint32_t par = st.vp[16 * u + 4 * j + t][(g & 3) * P / 4];
+      x[j] = pw[j] * param_scale(par);
+      a.zm = fmaf(pw[j], param_min(par), a.zm);
+    }
+    uint32_t bw[2];
+    split_weights(x, rest, bw, &got);
+    a.zo += got;
+    uint32_t v[4][NV];
 #pragma unroll
-    for (int i = 0; i < 4; ++i)                // channels 2i (row g) and 2i + 1 (row g + 8)
-      mma_bf16(a.c[4 * w + i], pair_of(l01, i), pair_of(h01, i), pair_of(l23, i), pair_of(h23, i), b0, b1);
+    for (int j = 0; j < 4; ++j) read_words<NV>(v[j], &st.v[16 * u + 4 * j + t][g * NV]);
+#pragma unroll
+    for (int w = 0; w < NV; ++w) {
+      // low halves: channels 0, 2, 4, 6 of the word; high halves: 1, 3, 5, 7
+      const uint32_t l01 = __byte_perm(v[0][w], v[1][w], 0x5410), h01 = __byte_perm(v[0][w], v[1][w], 0x7632);
+      const uint32_t l23 = __byte_perm(v[2][w], v[3][w], 0x5410), h23 = __byte_perm(v[2][w], v[3][w], 0x7632);
+#pragma unroll
+      for (int i = 0; i < 4; ++i)              // channels 2i (row g) and 2i + 1 (row g + 8)
+        mma_bf16(a.c[4 * w + i], pair_of(l01, i), pair_of(h01, i), pair_of(l23, i), pair_of(h23, i), bw[0], bw[1]);
+    }
   }
 }
 
-// The same with bf16 ring rows; rows are passed by address, at most n of 16
-// (key j of the tile is ring position pos0 + j).
+// ---- ring rows: bf16, kRingStep of them in a stage ------------------------------
+// 16-byte chunk c of row r (quarter c / (DH / 32) of the channels) lies at
+// chunk place(c) of its row, which spreads the lanes' reads over the banks.
 template <int DH>
-__device__ __forceinline__ void attend_ring(Acc<DH>& a, const __nv_bfloat16* kw, const __nv_bfloat16* vw, int pos0, int W,
-                                            const uint32_t (*qf)[2], float scale_log2, int n, int g, int t) {
-  constexpr int NW = Tile4<DH>::NW, NV = Tile4<DH>::NV;
-  float d[4] = {0.f, 0.f, 0.f, 0.f};
-  uint4 kr[2][NW];
+struct RingStage {
+  uint4 k[kRingStep][DH / 8];
+  uint4 v[kRingStep][DH / 8];
+};
+
+template <int DH>
+__device__ __forceinline__ int ring_place(int c, int r) {
+  constexpr int Q = DH / 32;                   // chunks per quarter
+  return (c / Q + 4 * (c % Q)) ^ (((r & 1) << 2) | ((r >> 1) & 3));
+}
+
+// Ring positions pos0 .. pos0 + n - 1 (n <= kRingStep, n <= W) into a stage;
+// the rest zero.
+template <int DH>
+__device__ __forceinline__ void fetch_ring(uint32_t stage, const __nv_bfloat16* kw, const __nv_bfloat16* vw, int pos0,
+                                           int W, int n, int lane) {
+  constexpr int NC = DH / 8;
+  const int first = pos0 % W;
 #pragma unroll
-  for (int r = 0; r < 2; ++r) {
-    const int key = g + 8 * r;
-#pragma unroll
-    for (int i = 0; i < NW; ++i)
-      kr[r][i] = key < n ? __ldcs(reinterpret_cast<const uint4*>(kw + (long long)((pos0 + key) % W) * DH + t * (DH / 4)) + i)
-                         : make_uint4(0u, 0u, 0u, 0u);
+  for (int i = 0; i < kRingStep * NC / 32; ++i) {
+    const int r = (i * 32 + lane) / NC, c = (i * 32 + lane) % NC;
+    const int row = r < n ? (first + r < W ? first + r : first + r - W) : 0;
+    const long long src = (long long)row * DH + c * 8;
+    const uint32_t dst = stage + (uint32_t)(r * NC + ring_place<DH>(c, r)) * 16;
+    cp_async<16>(dst, kw + src, r < n);
+    cp_async<16>(dst + (uint32_t)offsetof(RingStage<DH>, v), vw + src, r < n);
   }
-  uint4 vr[4][NV];
-#pragma unroll
-  for (int j = 0; j < 4; ++j)
-#pragma unroll
-    for (int i = 0; i < NV; ++i)
-      vr[j][i] = 4 * j + t < n
-                     ? __ldcs(reinterpret_cast<const uint4*>(vw + (long long)((pos0 + 4 * j + t) % W) * DH + g * (DH / 8)) + i)
-                     : make_uint4(0u, 0u, 0u, 0u);
+}
+
+// As attend_codes, with half an MMA tile's keys.
+template <int DH>
+__device__ __forceinline__ void attend_ring(Acc<DH>& a, const RingStage<DH>& st, const uint32_t (*qf)[2],
+                                            float scale_log2, int n, int g, int t) {
+  constexpr int NW = Lane<DH>::NW, NV = Lane<DH>::NV;
+  static_assert(kRingStep == 8, "keys g of the lanes");
+  float d[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
   for (int w = 0; w < NW; ++w) {
-    mma_bf16(d, kr[0][w].x, kr[1][w].x, kr[0][w].y, kr[1][w].y, qf[2 * w][0], qf[2 * w][1]);
-    mma_bf16(d, kr[0][w].z, kr[1][w].z, kr[0][w].w, kr[1][w].w, qf[2 * w + 1][0], qf[2 * w + 1][1]);
+    const uint4 k = st.k[g][ring_place<DH>(t * NW + w, g)];
+    mma_bf16(d, k.x, 0u, k.y, 0u, qf[2 * w][0], qf[2 * w][1]);
+    mma_bf16(d, k.z, 0u, k.w, 0u, qf[2 * w + 1][0], qf[2 * w + 1][1]);
   }
-  float s[2];
-#pragma unroll
-  for (int r = 0; r < 2; ++r) {
-    float x = d[2 * r] + d[2 * r + 1];
-    x += __shfl_xor_sync(0xffffffffu, x, 1);
-    s[r] = __shfl_sync(0xffffffffu, x, 0, 4) * scale_log2;
-  }
-  float p0, p1;
-  weigh(a, s[0], s[1], n, g, &p0, &p1);
-  float pw[4] = {__shfl_sync(0xffffffffu, p0, 4 * t), __shfl_sync(0xffffffffu, p0, 16 + 4 * t),
-                 __shfl_sync(0xffffffffu, p1, 4 * t), __shfl_sync(0xffffffffu, p1, 16 + 4 * t)};
-#pragma unroll
-  for (int j = 0; j < 4; ++j) pw[j] = part_of(pw[j], g);
-  const uint32_t b0 = pack_bf16x2(pw[0], pw[1]), b1 = pack_bf16x2(pw[2], pw[3]);
+  float s = d[0] + d[1], p, pw[4], got;
+  s += __shfl_xor_sync(0xffffffffu, s, 1);
+  s = __shfl_sync(0xffffffffu, s, 0, 4) * scale_log2;
+  if (g >= n) s = -INFINITY;
+  weigh<DH, 1>(a, &s, &p);
+  gather_weights(p, 0.f, t, pw);
+  uint32_t bw[2];
+  split_weights(pw, g < 4 ? 0.f : 1.f, bw, &got);
 #pragma unroll
   for (int w = 0; w < NV; ++w) {
-    const uint32_t y[4][4] = {{vr[0][w].x, vr[0][w].y, vr[0][w].z, vr[0][w].w},
-                              {vr[1][w].x, vr[1][w].y, vr[1][w].z, vr[1][w].w},
-                              {vr[2][w].x, vr[2][w].y, vr[2][w].z, vr[2][w].w},
-                              {vr[3][w].x, vr[3][w].y, vr[3][w].z, vr[3][w].w}};
+    const uint4 v0 = st.v[t][ring_place<DH>(g * NV + w, t)], v1 = st.v[4 + t][ring_place<DH>(g * NV + w, 4 + t)];
+    const uint32_t x[4] = {v0.x, v0.y, v0.z, v0.w}, y[4] = {v1.x, v1.y, v1.z, v1.w};
 #pragma unroll
     for (int i = 0; i < 4; ++i)
-      mma_bf16(a.c[4 * w + i], __byte_perm(y[0][i], y[1][i], 0x5410), __byte_perm(y[0][i], y[1][i], 0x7632),
-               __byte_perm(y[2][i], y[3][i], 0x5410), __byte_perm(y[2][i], y[3][i], 0x7632), b0, b1);
+      mma_bf16(a.c[4 * w + i], __byte_perm(x[i], y[i], 0x5410), __byte_perm(x[i], y[i], 0x7632), 0u, 0u, bw[0], bw[1]);
   }
 }
 
+static_assert(sizeof(RingStage<128>) <= sizeof(Stage<128>) && sizeof(RingStage<64>) <= sizeof(Stage<64>), "stage");
+
+__device__ __forceinline__ void prefetch_l2(const void* p) { asm volatile("prefetch.global.L2 [%0];" :: "l"(p)); }
+
 template <int DH>
-__global__ void __launch_bounds__(kThreads)
+__global__ void __launch_bounds__(kThreads, kCtasPerSm)
 decode_kernel(const Params pp) {
   const decode::Params& p = pp.d;
   constexpr int W8 = DH / 8, PG = DH / kGroup;
   constexpr int NQ = DH / 16;                  // score MMAs per tile
   constexpr int NE = kWarps + 1;               // merged entries: the warps and the query's own key
-  constexpr int kStride = kWarps * kTile;
 
   __shared__ __align__(16) float s_self[2][DH];
   __shared__ float s_m[NE], s_l[NE];
   __shared__ __align__(16) float s_acc[NE][DH];
   __shared__ int s_last;
+  extern __shared__ __align__(16) uint8_t s_stages[];    // Stage<DH>[kWarps][kStages]
 
   const int b = blockIdx.x / p.splits_per_b;
   const int rem = blockIdx.x - b * p.splits_per_b;
@@ -445,6 +606,106 @@ decode_kernel(const Params pp) {
     [[maybe_unused]] const long long n_ring = (long long)p.B * p.H * p.W * DH;
     const int warp = tid >> 5, lane = tid & 31, g = lane >> 2, tq = lane & 3;
 
+    // ---- the query, loaded ahead of the cache stream; then the recurrence's
+    // inputs are warmed (they are used after the stream) ----
+    const bool q_ok = RATP_IN(bh * DH, DH, n_tok);
+    uint4 qv[DH / 32];                         // this lane's quarter of the channels
+#pragma unroll
+    for (int i = 0; i < DH / 32; ++i)
+      qv[i] = q_ok ? reinterpret_cast<const uint4*>(p.q + bh * DH + tq * (DH / 4))[i] : make_uint4(0u, 0u, 0u, 0u);
+    if (split == 0 && q_ok && tid < 2 * DH / 32) {
+      // state rows (fp32, 128 bytes per thread), then x_k, x_v, g
+      const int st = tid / (DH / 32), c = tid % (DH / 32) * 32;
+      prefetch_l2(p.state + ((long long)st * p.B * p.H + bh) * DH + c);
+      prefetch_l2((st == 0 ? p.xk : p.xv) + bh * DH + c);
+      if (st == 0) prefetch_l2(p.g + bh * DH + c);
+    }
+    // ---- this split's share: units [u0, u1) of slots, then of ring keys ----
+    const long long u0 = (long long)split * p.split_keys, u1 = u0 + p.split_keys;
+    const int s_end = (int)min((long long)n_slots, u1);
+    const auto ring_at = [&](long long u) {
+      return (int)min((long long)n_win, (max(u - n_slots, 0ll) + kRingUnits - 1) / kRingUnits);
+    };
+    const int k0 = (int)min((long long)n_slots, u0) + warp * kStep;
+    Stage<DH>* const stages = reinterpret_cast<Stage<DH>*>(s_stages) + warp * kStages;
+    const uint32_t stage0 = (uint32_t)__cvta_generic_to_shared(stages);
+    // a warp's steps: rows k0 + i kRows .. of the cache, then its share of the
+    // ring; one commit group per step, empty past the end
+    constexpr int kRows = kWarps * kStep;
+    const int r_begin = ring_at(u0), r_end = RATP_IN(bh * p.W * DH, (long long)p.W * DH, n_ring) ? ring_at(u1) : 0;
+    const __nv_bfloat16* kw = p.Kw + bh * p.W * DH;
+    const __nv_bfloat16* vw = p.Vw + bh * p.W * DH;
+    Walk<DH> walk;
+    walk.start(kc, pp.Kp, vc, pp.Vp, row0 + k0, lane);
+    int at = k0, fill = 0;                     // next cached rows to fetch, and the stage for them
+    int ring = r_begin + warp * kRingStep;     // next ring rows, after the cached ones
+    auto fetch_next = [&]() {
+      const uint32_t stage = stage0 + fill * (uint32_t)sizeof(Stage<DH>);
+      if (at < s_end) {
+        const int n = min(kStep, s_end - at);
+        if (RATP_IN(row0 + at, n, n_rows)) walk.fetch(stage, n, lane);
+        walk.advance(kRows);
+        at += kRows;
+      } else if (ring < r_end) {
+        fetch_ring<DH>(stage, kw, vw, w_lo + ring, p.W, min(kRingStep, r_end - ring), lane);
+        ring += kWarps * kRingStep;
+      }
+      asm volatile("cp.async.commit_group;" ::: "memory");
+      fill = fill + 1 == kStages ? 0 : fill + 1;
+    };
+#pragma unroll
+    for (int i = 0; i < kStages - 1; ++i) fetch_next();
+
+    uint32_t qf[NQ][2];
+    float qsum[2];
+    {
+      float sum = 0.f;
+#pragma unroll
+      for (int i = 0; i < DH / 32; ++i) {
+        float f[8];
+        Elem<__nv_bfloat16>::unpack(qv[i], f);
+#pragma unroll
+        for (int j = 0; j < 8; ++j) sum += f[j];
+        const bool mine = g == tq;             // B's column n = g is quarter n alone
+        qf[2 * i][0] = mine ? qv[i].x : 0u;
+        qf[2 * i][1] = mine ? qv[i].y : 0u;
+        qf[2 * i + 1][0] = mine ? qv[i].z : 0u;
+        qf[2 * i + 1][1] = mine ? qv[i].w : 0u;
+      }
+      qsum[0] = __shfl_sync(0xffffffffu, sum, 2 * tq, 4);          // quarters 2t, 2t + 1
+      qsum[1] = __shfl_sync(0xffffffffu, sum, 2 * tq + 1, 4);
+      if (tq >= 2) qsum[0] = qsum[1] = 0.f;
+    }
+
+    Acc<DH> a;
+    a.m = -INFINITY;
+    a.l = 0.f;
+    a.zm = a.zo = 0.f;
+#pragma unroll
+    for (int j = 0; j < NQ; ++j)
+#pragma unroll
+      for (int i = 0; i < 4; ++i) a.c[j][i] = 0.f;
+
+    int use = 0;
+    for (int k = k0; k < s_end; k += kRows) {
+      fetch_next();
+      asm volatile("cp.async.wait_group %0;" :: "n"(kStages - 1) : "memory");
+      __syncwarp();
+      attend_codes<DH>(a, stages[use], qf, qsum, p.scale_log2, s_end - k, g, tq);
+      __syncwarp();
+      use = use + 1 == kStages ? 0 : use + 1;
+    }
+    for (int r = r_begin + warp * kRingStep; r < r_end; r += kWarps * kRingStep) {
+      fetch_next();
+      asm volatile("cp.async.wait_group %0;" :: "n"(kStages - 1) : "memory");
+      __syncwarp();
+      attend_ring<DH>(a, reinterpret_cast<const RingStage<DH>&>(stages[use]), qf, p.scale_log2, min(kRingStep, r_end - r),
+                      g, tq);
+      __syncwarp();
+      use = use + 1 == kStages ? 0 : use + 1;
+    }
+
+    // ---- the recurrence, the appended row ----
     if (split == 0) {
       decode::recurrence_step<DH>(p, bh, t, s_self[0], s_self[1], [](int, int, __nv_bfloat16) {});
       if (t % Dd == Dd - 1) {
@@ -454,84 +715,25 @@ decode_kernel(const Params pp) {
           // 8 channels per thread; W8 threads per stream, in whole groups of 4
           const int st = tid / W8, w = tid % W8;
           uint32_t par;
-          const uint32_t code = quantise8(&s_self[st][8 * w], &par, 0xfu << (lane & ~3));
+          float2 f[4];
+#pragma unroll
+          for (int i = 0; i < 4; ++i) f[i] = *reinterpret_cast<const float2*>(&s_self[st][8 * w + 2 * i]);
+          const uint32_t code = quantise8(Elem<__nv_bfloat16>::pack2(f), &par, 0xfu << (lane & ~3));
           (st == 0 ? kc : vc)[(row0 + app_slot) * W8 + w] = code;
           if ((w & 3) == 0) (st == 0 ? pp.Kp : pp.Vp)[(row0 + app_slot) * PG + w / 4] = par;
         }
       }
     }
 
-    // ---- the query: fragments of this lane's channel quarter, quarter sums ----
-    uint32_t qf[NQ][2];
-    float qsum[2];
-    const bool q_ok = RATP_IN(bh * DH, DH, n_tok);
-    {
-      const uint4* q4 = reinterpret_cast<const uint4*>(p.q + bh * DH + tq * (DH / 4));
-      float sum = 0.f;
-#pragma unroll
-      for (int i = 0; i < DH / 32; ++i) {
-        const uint4 v = q_ok ? q4[i] : make_uint4(0u, 0u, 0u, 0u);
-        float f[8];
-        Elem<__nv_bfloat16>::unpack(v, f);
-#pragma unroll
-        for (int j = 0; j < 8; ++j) sum += f[j];
-        const bool mine = g == tq;             // B's column n = g is quarter n alone
-        qf[2 * i][0] = mine ? v.x : 0u;
-        qf[2 * i][1] = mine ? v.y : 0u;
-        qf[2 * i + 1][0] = mine ? v.z : 0u;
-        qf[2 * i + 1][1] = mine ? v.w : 0u;
-      }
-      qsum[0] = __shfl_sync(0xffffffffu, sum, 2 * tq, 4);          // quarters 2t, 2t + 1 (used by t < 2)
-      qsum[1] = __shfl_sync(0xffffffffu, sum, 2 * tq + 1, 4);
-    }
-
-    Acc<DH> a;
-    a.m = -INFINITY;
-    a.l = 0.f;
-    a.z = 0.f;
-#pragma unroll
-    for (int j = 0; j < NQ; ++j)
-#pragma unroll
-      for (int i = 0; i < 4; ++i) a.c[j][i] = 0.f;
-
-    // ---- this split's share: units [u0, u1) of slots, then of ring keys ----
-    const long long u0 = (long long)split * p.split_keys, u1 = u0 + p.split_keys;
-    const int s_end = (int)min((long long)n_slots, u1);
-    const auto ring_at = [&](long long u) {
-      return (int)min((long long)n_win, (max(u - n_slots, 0ll) + kRingUnits - 1) / kRingUnits);
-    };
-    int k = (int)min((long long)n_slots, u0) + warp * kTile;
-    Tile4<DH> cur;
-    auto load = [&](Tile4<DH>& f, int at) {
-      int n = min(kTile, s_end - at);
-      if (!RATP_IN(row0 + at, max(n, 0), n_rows)) n = 0;
-      load_tile<DH>(f, kc + (row0 + at) * W8, pp.Kp + (row0 + at) * PG, vc + (row0 + at) * W8,
-                    pp.Vp + (row0 + at) * PG, n, g, tq);
-    };
-    if (k < s_end) load(cur, k);
-    while (k < s_end) {
-      Tile4<DH> next;
-      const int kn = k + kStride;
-      if (kn < s_end) load(next, kn);
-      attend_codes<DH>(a, cur, qf, qsum, p.scale_log2, min(kTile, s_end - k), g, tq);
-      cur = next;
-      k = kn;
-    }
-    const int r_end = ring_at(u1);
-    if (n_win > 0 && RATP_IN(bh * p.W * DH, (long long)p.W * DH, n_ring)) {
-      const __nv_bfloat16* kw = p.Kw + bh * p.W * DH;
-      const __nv_bfloat16* vw = p.Vw + bh * p.W * DH;
-      for (int r = ring_at(u0) + warp * kTile; r < r_end; r += kStride)
-        attend_ring<DH>(a, kw, vw, w_lo + r, p.W, qf, p.scale_log2, min(kTile, r_end - r), g, tq);
-    }
-
     // ---- this warp's entry ----
 #pragma unroll
     for (int off = 4; off < 32; off <<= 1) a.l += __shfl_xor_sync(0xffffffffu, a.l, off);
-    a.z += __shfl_xor_sync(0xffffffffu, a.z, 1);
-    a.z += __shfl_xor_sync(0xffffffffu, a.z, 2);
-    a.z += __shfl_xor_sync(0xffffffffu, a.z, 16);                  // lanes g and g + 4: quarter g % 4
-    const float z = __shfl_sync(0xffffffffu, a.z, (g >> 1) << 2);  // of the quarter this lane's channels lie in
+    // minima count once (columns 0..3); the offsets of both parts
+    float z = fmaf(-128.f, a.zo, g < 4 ? a.zm : 0.f);
+    z += __shfl_xor_sync(0xffffffffu, z, 1);
+    z += __shfl_xor_sync(0xffffffffu, z, 2);
+    z += __shfl_xor_sync(0xffffffffu, z, 16);                      // lanes g and g + 4: quarter g % 4
+    z = __shfl_sync(0xffffffffu, z, (g >> 1) << 2);                // of the quarter this lane's channels lie in
     if (lane == 0) { s_m[warp] = a.m; s_l[warp] = a.l; }
 #pragma unroll
     for (int j = 0; j < NQ; ++j) {
@@ -550,10 +752,15 @@ decode_kernel(const Params pp) {
       float s = -INFINITY;
       if (split == 0) {
         s = 0.f;
-        if (q_ok)
-          for (int c = lane; c < DH; c += 32) s = fmaf(__bfloat162float(p.q[bh * DH + c]), s_self[0][c], s);
 #pragma unroll
-        for (int off = 16; off > 0; off >>= 1) s += __shfl_xor_sync(0xffffffffu, s, off);
+        for (int i = 0; i < DH / 32; ++i) {
+          float f[8];
+          Elem<__nv_bfloat16>::unpack(qv[i], f);
+#pragma unroll
+          for (int j = 0; j < 8; ++j) s = fmaf(f[j], s_self[0][tq * (DH / 4) + 8 * i + j], s);
+        }
+        s += __shfl_xor_sync(0xffffffffu, s, 1);       // the 4 quarters; every g computes the same
+        s += __shfl_xor_sync(0xffffffffu, s, 2);
         s *= p.scale_log2;
       }
       if (lane == 0) { s_m[kWarps] = s; s_l[kWarps] = split == 0 ? 1.f : 0.f; }

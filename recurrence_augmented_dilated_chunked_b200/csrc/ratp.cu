@@ -548,8 +548,27 @@ long long split_units(bool dense, int T_max, int D, int W, int kv_bits) {
 // wave of CTAs (kDecodeCtasPerSm resident per SM), never below kMinSplitKeys.
 constexpr int kDecodeCtasPerSm = 6;
 constexpr int kMinSplitKeys = 128;
-constexpr int kDecodeCtasPerSmQ4 = 4;
-constexpr int kMinSplitKeysQ4 = 256;
+// A 4-bit step: the split whose waves of resident CTAs cost least, a CTA
+// costing its keys and kQ4CtaKeys more (start, merge), in units of 4-bit rows.
+constexpr long long kQ4CtaKeys = 256;
+constexpr int kQ4MaxSplits = 64;
+
+long long q4_split(int B, int H, int T_max, int D, int W, const uint8_t* head_mask, long long max_keys) {
+  const long long slots = (long long)sm_count() * decode_q4::kCtasPerSm;
+  long long best = std::max(max_keys, 1ll), best_cost = 0;
+  for (int n = 1; n <= kQ4MaxSplits; ++n) {
+    const long long split = (max_keys + n - 1) / n;
+    if (n > 1 && split < kQ4CtaKeys) break;
+    long long ctas = 0;
+    for (int h = 0; h < H; ++h) {
+      const long long keys = split_units(head_mask != nullptr && head_mask[h] != 0, T_max, D, W, 4);
+      ctas += std::max(1ll, (keys + split - 1) / std::max(split, 1ll));
+    }
+    const long long cost = (ctas * B + slots - 1) / slots * (split + kQ4CtaKeys);
+    if (n == 1 || cost < best_cost) { best = std::max(split, 1ll); best_cost = cost; }
+  }
+  return best;
+}
 
 int cache_layout(int B, int H, int Dh, int T_max, int D, int W, const uint8_t* head_mask,
                  int kv_bits, CacheLayout* L) {
@@ -557,7 +576,6 @@ int cache_layout(int B, int H, int Dh, int T_max, int D, int W, const uint8_t* h
   if (Dh != 128 && Dh != 64) return RATP_ERR_SHAPE;
   if (H > RATP_MAX_HEADS) return RATP_ERR_SHAPE;
   const bool q4 = kv_bits == 4;
-  const long long min_split = q4 ? kMinSplitKeysQ4 : kMinSplitKeys;
   long long per_b = 0, keys_total = 0, max_keys = 0;
   for (int h = 0; h < H; ++h) {
     const bool dense = head_mask != nullptr && head_mask[h] != 0;
@@ -567,14 +585,14 @@ int cache_layout(int B, int H, int Dh, int T_max, int D, int W, const uint8_t* h
     if (keys > max_keys) max_keys = keys;
   }
   L->rows_per_b = per_b;
-  const long long target_ctas = (long long)sm_count() * (q4 ? kDecodeCtasPerSmQ4 : kDecodeCtasPerSm);
+  const long long target_ctas = (long long)sm_count() * kDecodeCtasPerSm;
   long long split = (keys_total + target_ctas - 1) / target_ctas;
-  if (split < min_split) split = min_split;
+  if (split < kMinSplitKeys) split = kMinSplitKeys;
   // Keep every head's split count but even out its splits: the split becomes
   // the largest per-split share among the heads, so no CTA streams more keys
   // than it must (7.6B hybrid: 357 -> 347 keys, 24 and 6 splits per head).
   {
-    long long even = min_split;
+    long long even = kMinSplitKeys;
     for (int h = 0; h < H; ++h) {
       const bool dense = head_mask != nullptr && head_mask[h] != 0;
       const long long keys = split_units(dense, T_max, D, W, kv_bits);
@@ -584,6 +602,7 @@ int cache_layout(int B, int H, int Dh, int T_max, int D, int W, const uint8_t* h
     }
     split = std::min(split, even);
   }
+  if (q4) split = q4_split(B, H, T_max, D, W, head_mask, max_keys);
   if (split > (1 << 30)) split = 1 << 30;
   L->split_keys = (int)split;
   L->max_splits = (int)((max_keys + L->split_keys - 1) / L->split_keys);
@@ -1018,8 +1037,8 @@ int ratp_cache_init_q4(ratp_cache* c, void* buffer, size_t bytes, int B, int H, 
 int ratp_cache_read_q4(const ratp_cache* c, float* k, float* v, void* stream) {
   if (!c || c->kv_bits != 4) return RATP_ERR_ARG;
   if ((k && !aligned16(k)) || (v && !aligned16(v))) return RATP_ERR_ALIGN;
-  const long long words = (long long)c->B * c->rows_per_b * (c->Dh / 8);
-  const long long grid = (words + 255) / 256;
+  const long long quads = (long long)c->B * c->rows_per_b * (c->Dh / 4);
+  const long long grid = (quads + 256 * decode_q4::kReadPer - 1) / (256 * decode_q4::kReadPer);
   if (grid == 0) return RATP_OK;
   if (grid > 0x7fffffffll) return RATP_ERR_SHAPE;
   cudaStream_t st = static_cast<cudaStream_t>(stream);
@@ -1029,7 +1048,7 @@ int ratp_cache_read_q4(const ratp_cache* c, float* k, float* v, void* stream) {
   for (int i = 0; i < 2; ++i) {
     if (out[i] == nullptr) continue;
     decode_q4::unpack_kernel<<<(unsigned)grid, 256, 0, st>>>(static_cast<const uint32_t*>(codes[i]),
-                                                             static_cast<const uint32_t*>(par[i]), out[i], words);
+                                                             static_cast<const uint32_t*>(par[i]), out[i], quads);
     const int rc = launch_status();
     if (rc) return rc;
   }
@@ -1067,8 +1086,17 @@ int ratp_cache_pack(ratp_cache* c, const void* hk, const void* hv, int T, void* 
     p4.d = p;
     p4.Kp = static_cast<uint32_t*>(c->Kp);
     p4.Vp = static_cast<uint32_t*>(c->Vp);
-    if (c->Dh == 128) decode_q4::pack_kernel<128><<<grid, 256, 0, st>>>(p4);
-    else decode_q4::pack_kernel<64><<<grid, 256, 0, st>>>(p4);
+    p4.base[0] = 0;
+    for (int h = 0; h < c->H; ++h) {
+      const int rows = T / (c->dense[h] ? 1 : c->D) + (c->W > 0 ? (T < c->W ? T : c->W) : 0);
+      const int per = rpb * decode_q4::kPackRows;
+      p4.base[h + 1] = p4.base[h] + (rows + per - 1) / per;
+    }
+    if (p4.base[c->H] == 0) p4.base[c->H] = 1;   // still sets len
+    const long long blocks = (long long)p4.base[c->H] * c->B;
+    if (blocks > 0x7fffffffll) return RATP_ERR_SHAPE;
+    if (c->Dh == 128) decode_q4::pack_kernel<128><<<(unsigned)blocks, 256, 0, st>>>(p4);
+    else decode_q4::pack_kernel<64><<<(unsigned)blocks, 256, 0, st>>>(p4);
   } else if (c->Dh == 128) {
     decode::pack_kernel<128><<<grid, 256, 0, st>>>(p);
   } else {
@@ -1201,8 +1229,12 @@ int decode_launch(const void* q, const void* xk, const void* xv, const void* g,
     p4.d = p;
     p4.Kp = static_cast<uint32_t*>(c->Kp);
     p4.Vp = static_cast<uint32_t*>(c->Vp);
-    e = (c->Dh == 128) ? cudaLaunchKernelEx(&cfg, decode_q4::decode_kernel<128>, p4)
-                       : cudaLaunchKernelEx(&cfg, decode_q4::decode_kernel<64>, p4);
+    const int smem = decode_q4::kWarps * decode_q4::kStages *
+                     (int)(c->Dh == 128 ? sizeof(decode_q4::Stage<128>) : sizeof(decode_q4::Stage<64>));
+    cfg.dynamicSmemBytes = smem;
+    auto kernel = c->Dh == 128 ? decode_q4::decode_kernel<128> : decode_q4::decode_kernel<64>;
+    if (!ensure_smem(kernel, smem)) return RATP_ERR_CUDA;
+    e = cudaLaunchKernelEx(&cfg, kernel, p4);
   } else {
     e = (c->Dh == 128) ? cudaLaunchKernelEx(&cfg, decode::decode_kernel<128>, p)
                        : cudaLaunchKernelEx(&cfg, decode::decode_kernel<64>, p);
