@@ -362,6 +362,40 @@ int ratp_qk_norm_rope(const ratp_view* q, const ratp_view* k, const ratp_view* q
                       int B, int T, int Dh, int rot, int interleaved, float eps, int dtype, void* stream);
 
 /* ------------------------------------------------------------------------
+ * Linear attention with a decay for each head: the mixer of a layer whose
+ * state has a fixed size, beside the dilated layers of a stack (the write-up's
+ * section 6 mixes layer kinds; this kind is not one of its own).
+ *
+ *   S_t = exp(log_decay[h]) * S_{t-1} + k_t v_t^T     (Dh x Dh per (b, h), fp32)
+ *   o_t = scale * q_t S_t
+ *
+ * q, k, v, o: bf16 [B][T][H][Dh] (step: [B][H][Dh]), Dh 64 or 128.
+ * log_decay: fp32 [H], values <= 0 (0: no decay; -inf: no memory).
+ * initial_state: fp32 [B][H][Dh][Dh] (row: channel of k, column: channel of v)
+ *   before the first token; NULL = zero.  final_state: the state after the
+ *   last token, or NULL; it may be initial_state itself (in place).  A prefill
+ *   that starts from another's final_state continues it.
+ * ratp_linear_attn_prefill runs chunks of 128 tokens on the tensor cores
+ *   (sequences of at most 16 tokens run token by token); P and the state enter
+ *   the output's products as bf16, the state itself is advanced in fp32.
+ * workspace: device scratch of ratp_linear_attn_workspace_bytes bytes (0 where
+ *   the (b, h) alone fill the GPU), 16-byte aligned, no initialisation; calls
+ *   sharing one must be ordered on one stream.
+ * ratp_linear_attn_step: one token per sequence, state updated in place.
+ * Errors: ARG (null pointer, negative size, scale not finite), SHAPE (Dh, H *
+ *   B * tokens too large), ALIGN, CAPACITY (workspace too small), UNSUPPORTED
+ *   (dtype not bf16).  B, T or H == 0 is a no-op (final_state is then left as
+ *   it is).
+ * ---------------------------------------------------------------------- */
+int ratp_linear_attn_workspace_bytes(int B, int T, int H, int Dh, size_t* bytes);
+int ratp_linear_attn_prefill(const void* q, const void* k, const void* v, const float* log_decay,
+                             const float* initial_state, float* final_state, void* o,
+                             int B, int T, int H, int Dh, float scale, int dtype,
+                             void* workspace, size_t workspace_bytes, void* stream);
+int ratp_linear_attn_step(const void* q, const void* k, const void* v, const float* log_decay,
+                          float* state, void* o, int B, int H, int Dh, float scale, int dtype, void* stream);
+
+/* ------------------------------------------------------------------------
  * D-compressed KV cache and decode (RAT+ abstract: the KV cache shrinks by D).
  *
  * Layout (all bf16 rows of Dh elements):

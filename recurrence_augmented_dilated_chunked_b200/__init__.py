@@ -19,6 +19,9 @@ from ._binding import (  # noqa: F401
     exported_symbols,
     guard_line,
     last_error,
+    linear_attn_prefill,
+    linear_attn_step,
+    linear_attn_workspace_bytes,
     load_library,
     prefill_fused,
     prefill_fused_workspace,

@@ -92,6 +92,9 @@ _SIGS = {
     "ratp_prefill_fused_workspace_bytes": ([_I, _I, _I, _I, ctypes.POINTER(_SZ)], _I),
     "ratp_prefill_fused": ([_P, _P, _P, _P, _P, _P, _P, _P, _I, _I, _I, _I, _I, _I, _P, _I, _P, _SZ, _P], _I),
     "ratp_qk_norm_rope": ([ctypes.POINTER(ViewStruct)] * 4 + [_P] * 4 + [_I] * 6 + [ctypes.c_float, _I, _P], _I),
+    "ratp_linear_attn_workspace_bytes": ([_I, _I, _I, _I, ctypes.POINTER(_SZ)], _I),
+    "ratp_linear_attn_prefill": ([_P] * 7 + [_I] * 4 + [ctypes.c_float, _I, _P, _SZ, _P], _I),
+    "ratp_linear_attn_step": ([_P] * 6 + [_I] * 3 + [ctypes.c_float, _I, _P], _I),
     "ratp_cache_bytes_q4": ([_I, _I, _I, _I, _I, _I, _P, ctypes.POINTER(_SZ)], _I),
     "ratp_cache_init_q4": ([ctypes.POINTER(CacheStruct), _P, _SZ, _I, _I, _I, _I, _I, _I, _P, _P], _I),
     "ratp_cache_read_q4": ([ctypes.POINTER(CacheStruct), _P, _P, _P], _I),
@@ -136,6 +139,28 @@ def _check(fn, code):
 
 def _stream(t: torch.Tensor):
     return ctypes.c_void_p(torch.cuda.current_stream(t.device).cuda_stream)
+
+
+class _on:
+    """Makes ``device`` current inside the block (nothing to do, and nothing
+    paid, where it is already)."""
+
+    def __init__(self, device):
+        self.index = device.index
+
+    def __enter__(self):
+        self.guard = None
+        if self.index is not None and self.index != torch.cuda.current_device():
+            self.guard = torch.cuda.device(self.index)
+            self.guard.__enter__()
+
+    def __exit__(self, *exc):
+        if self.guard is not None:
+            self.guard.__exit__(*exc)
+
+
+def _addr(t):
+    return None if t is None else t.data_ptr()
 
 
 def _ptr(t):
@@ -493,12 +518,81 @@ def qk_norm_rope(q, k, q_weight, k_weight, inv_freq, positions=None, eps=1e-6, i
         if positions.device != dev or tuple(positions.shape) not in ((B,), (B, T)):
             raise ValueError("positions must be int32 [B] or [B, T] on %s" % dev)
         per_token = 1 if positions.dim() == 2 else 0
-    with torch.cuda.device(dev):
+    with _on(dev):
         _check("ratp_qk_norm_rope", lib.ratp_qk_norm_rope(
             views[0][0], views[1][0], views[0][1], views[1][1], _ptr(q_weight if q is not None else None),
             _ptr(k_weight if k is not None else None), _ptr(inv_freq), _ptr(positions), per_token, B, T, Dh, rot,
             1 if interleaved else 0, float(eps), _DTYPE[dt], _stream(ref)))
     return tuple(outs)
+
+
+def _linear_args(q, k, v, log_decay, states, out, dims):
+    if not isinstance(q, torch.Tensor) or q.dim() != dims:
+        raise ValueError("q must be a CUDA tensor of %d dimensions" % dims)
+    if out is None:
+        out = torch.empty_like(q)
+    for t, nm in ((q, "q"), (k, "k"), (v, "v"), (out, "out")):
+        _need(t, nm, torch.bfloat16)
+        if t.shape != q.shape or t.device != q.device:
+            raise ValueError("q, k, v and out must have one shape, on one device")
+    B, H, Dh = q.shape[0], q.shape[-2], q.shape[-1]
+    _need(log_decay, "log_decay", torch.float32)
+    if log_decay.shape != (H,) or log_decay.device != q.device:
+        raise ValueError("log_decay must be [H] on %s" % q.device)
+    for s, nm in states:
+        if s is not None:
+            _need(s, nm, torch.float32)
+            if s.shape != (B, H, Dh, Dh) or s.device != q.device:
+                raise ValueError("%s must be [B, H, Dh, Dh] on %s" % (nm, q.device))
+    return out
+
+
+def linear_attn_prefill(q, k, v, log_decay, initial_state=None, final_state=None, scale=None, out=None,
+                        workspace=None):
+    """Linear attention with a decay for each head over [B, T, H, Dh] (bf16, Dh
+    64 or 128): S_t = exp(log_decay[h]) S_{t-1} + k_t v_t^T, o_t = scale q_t S_t.
+
+    log_decay: fp32 [H], <= 0.  initial_state: fp32 [B, H, Dh, Dh] before the
+    first token (None: zero); final_state: receives the state after the last
+    one, and may be initial_state itself.  scale: Dh ** -0.5 by default.
+    workspace: uint8 tensor of ``linear_attn_workspace_bytes`` (default: one
+    from the current stream's allocator, so that no two calls or captured
+    graphs share one)."""
+    lib = load_library()
+    out = _linear_args(q, k, v, log_decay, ((initial_state, "initial_state"), (final_state, "final_state")), out, 4)
+    B, T, H, Dh = q.shape
+    with _on(q.device):
+        if workspace is None:
+            n = linear_attn_workspace_bytes(B, T, H, Dh)
+            workspace = torch.empty(n, dtype=torch.uint8, device=q.device) if n else None
+        _check("ratp_linear_attn_prefill", lib.ratp_linear_attn_prefill(
+            q.data_ptr(), k.data_ptr(), v.data_ptr(), log_decay.data_ptr(), _addr(initial_state), _addr(final_state),
+            out.data_ptr(), B, T, H, Dh, Dh ** -0.5 if scale is None else scale, RATP_BF16, _addr(workspace),
+            workspace.numel() if workspace is not None else 0, _stream(q)))
+    return out
+
+
+def linear_attn_workspace_bytes(B, T, H, Dh) -> int:
+    """Bytes of device scratch that one ``linear_attn_prefill`` of this shape needs."""
+    n = ctypes.c_size_t()
+    _check("ratp_linear_attn_workspace_bytes",
+           load_library().ratp_linear_attn_workspace_bytes(B, T, H, Dh, ctypes.byref(n)))
+    return n.value
+
+
+def linear_attn_step(q, k, v, log_decay, state, scale=None, out=None):
+    """One token per sequence of ``linear_attn_prefill``'s recurrence: q, k, v
+    bf16 [B, H, Dh]; state fp32 [B, H, Dh, Dh], updated in place."""
+    lib = load_library()
+    if state is None:
+        raise ValueError("state must be a CUDA tensor")
+    out = _linear_args(q, k, v, log_decay, ((state, "state"),), out, 3)
+    B, H, Dh = q.shape
+    with _on(q.device):
+        _check("ratp_linear_attn_step", lib.ratp_linear_attn_step(
+            q.data_ptr(), k.data_ptr(), v.data_ptr(), log_decay.data_ptr(), state.data_ptr(), out.data_ptr(), B, H, Dh,
+            Dh ** -0.5 if scale is None else scale, RATP_BF16, _stream(q)))
+    return out
 
 
 def last_error(device=None):
@@ -562,7 +656,7 @@ class KVCache:
         4-bit cache the fp32 values that the held rows stand for."""
         if self.kv_bits == 4:
             out = torch.empty(self.B, self.c.rows_per_b, self.Dh, dtype=torch.float32, device=self.buffer.device)
-            with torch.cuda.device(out.device):
+            with _on(out.device):
                 _check("ratp_cache_read_q4", load_library().ratp_cache_read_q4(
                     ctypes.byref(self.c), _ptr(out) if which == "k" else None,
                     None if which == "k" else _ptr(out), _stream(out)))

@@ -9,6 +9,7 @@
 //   decode_q4.cuh  the same over a cache whose dilated rows are held in 4 bits
 //   window.cuh     fixed look-back recurrence (window of the last L tokens)
 //   norm_rope.cuh  RMS norm of q and k heads with the rotary position
+//   linear_attn.cuh  linear attention with a decay per head (chunked, recurrent)
 #include <cuda.h>
 #include <cuda_runtime.h>
 #include <string.h>
@@ -40,6 +41,7 @@ __global__ void guard_probe_kernel() {
 #include "decode.cuh"
 #include "decode_q4.cuh"
 #include "norm_rope.cuh"
+#include "linear_attn.cuh"
 
 using namespace ratp;
 
@@ -530,6 +532,113 @@ int check_view(const ratp_view* v, int heads, int esize) {
   return RATP_OK;
 }
 
+// ---- linear attention -----------------------------------------------------------
+struct LinearPlan {
+  int n_chunks, seg_chunks, n_seg;
+};
+
+// Chunks per segment.  One pass over a segment's chunks with output costs
+// about 2 us per chunk, the pass for its state alone 1 us, a CTA's start and
+// end 3 us and the extra launches 4 us; the plan is the cheapest number of
+// segments under that model (128 (b, h) of 64 chunks: one segment each; 32 of
+// 128 chunks: four).
+int linear_plan(int B, int T, int H, int Dh, LinearPlan* pl) {
+  if (B < 0 || T < 0 || H < 0) return RATP_ERR_ARG;
+  if (Dh != 64 && Dh != 128) return RATP_ERR_SHAPE;
+  pl->n_chunks = (int)(((long long)T + linear_attn::C - 1) / linear_attn::C);
+  pl->seg_chunks = std::max(1, pl->n_chunks);
+  pl->n_seg = 1;
+  const long long pairs = (long long)B * H;
+  if (pairs == 0 || T <= linear_attn::kRecurrentTokens) return RATP_OK;
+  if (pairs > (1 << 20)) return RATP_ERR_SHAPE;
+  const long long slots = sm_count();
+  long long best = 0;
+  for (int want = 1; want <= std::min(pl->n_chunks, 256); ++want) {
+    const int sc = (pl->n_chunks + want - 1) / want, ns = (pl->n_chunks + sc - 1) / sc;
+    if (ns != want) continue;
+    long long cost = (pairs * ns + slots - 1) / slots * (2 * sc + 3);
+    if (ns > 1) cost += (pairs * (ns - 1) + slots - 1) / slots * (sc + 3) + 4;
+    if (want == 1 || cost < best) {
+      best = cost;
+      pl->seg_chunks = sc;
+      pl->n_seg = ns;
+    }
+    if (pairs * want > 4 * slots) break;
+  }
+  return RATP_OK;
+}
+
+size_t linear_ws_bytes(const LinearPlan& pl, int B, int H, int Dh) {
+  return pl.n_seg > 1 ? (size_t)B * H * pl.n_seg * Dh * Dh * 4 : 0;
+}
+
+int check_linear(const void* q, const void* k, const void* v, const float* ld, const float* init, const float* fin,
+                 const void* o, float scale, int dtype) {
+  if (dtype != RATP_BF16) return dtype == RATP_F32 ? RATP_ERR_UNSUPPORTED : RATP_ERR_ARG;
+  if (!(fabsf(scale) <= 3.0e38f)) return RATP_ERR_ARG;
+  if (!q || !k || !v || !ld || !o) return RATP_ERR_ARG;
+  for (const void* x : {q, k, v, o, static_cast<const void*>(init), static_cast<const void*>(fin)})
+    if (x != nullptr && !aligned16(x)) return RATP_ERR_ALIGN;
+  if ((reinterpret_cast<uintptr_t>(ld) & 3u) != 0) return RATP_ERR_ALIGN;
+  return RATP_OK;
+}
+
+int launch_linear_recurrent(const void* q, const void* k, const void* v, const float* ld, const float* init, float* fin,
+                            void* o, int B, int T, int H, int Dh, float scale, cudaStream_t st) {
+  linear_attn::RecurrentParams p;
+  p.q = static_cast<const __nv_bfloat16*>(q);
+  p.k = static_cast<const __nv_bfloat16*>(k);
+  p.v = static_cast<const __nv_bfloat16*>(v);
+  p.o = static_cast<__nv_bfloat16*>(o);
+  p.log_decay = ld; p.init = init; p.fin = fin;
+  p.B = B; p.T = T; p.H = H; p.scale = scale;
+  const long long grid = (long long)B * H * (Dh / 64);
+  if (grid > 0x7fffffffll) return RATP_ERR_SHAPE;
+  if (Dh == 128) linear_attn::recurrent_kernel<128><<<(unsigned)grid, 256, 0, st>>>(p);
+  else linear_attn::recurrent_kernel<64><<<(unsigned)grid, 256, 0, st>>>(p);
+  return launch_status();
+}
+
+// [B][T][H][Dh] bf16, box of 64 channels of one head x 128 tokens, 128-byte swizzle
+bool make_chunk_map(CUtensorMap* m, const void* base, int B, int T, int H, int Dh) {
+  EncodeTiledFn fn = encode_fn();
+  if (!fn) return false;
+  const cuuint64_t dims[4] = {(cuuint64_t)Dh, (cuuint64_t)H, (cuuint64_t)T, (cuuint64_t)B};
+  const cuuint64_t row = (cuuint64_t)H * Dh * 2;
+  const cuuint64_t strides[3] = {(cuuint64_t)Dh * 2, row, row * T};
+  const cuuint32_t box[4] = {64, 1, linear_attn::C, 1};
+  const cuuint32_t estr[4] = {1, 1, 1, 1};
+  return fn(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, const_cast<void*>(base), dims, strides, box, estr,
+            CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+            CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+template <int DH>
+int launch_linear_chunks(const LinearPlan& pl, const CUtensorMap& tq, const CUtensorMap& tk, const CUtensorMap& tv,
+                         const linear_attn::Params& p, cudaStream_t st) {
+  using namespace linear_attn;
+  constexpr int smem = (int)Layout<DH>::kBytes;
+  const long long pairs = (long long)p.B * p.H;
+  if (pl.n_seg > 1) {
+    if (!ensure_smem(chunk_kernel<DH, false>, smem)) return RATP_ERR_CUDA;
+    chunk_kernel<DH, false><<<(unsigned)(pairs * (pl.n_seg - 1)), kThreads, smem, st>>>(tq, tk, tv, p);
+    int rc = launch_status();
+    if (rc) return rc;
+    const int quads = DH * DH / 4;
+    for (long long at = 0; at < pairs; at += 65535) {      // grid.y limit
+      const int n = (int)std::min(65535ll, pairs - at);
+      combine_kernel<<<dim3((unsigned)((quads + 255) / 256), (unsigned)n), 256, 0, st>>>(
+          p.ws + (size_t)at * pl.n_seg * DH * DH, p.init != nullptr ? p.init + (size_t)at * DH * DH : nullptr,
+          p.log_decay, p.H, (int)(at % p.H), pl.n_seg, quads, pl.seg_chunks * C, (pairs - at) * pl.n_seg * DH * DH);
+      rc = launch_status();
+      if (rc) return rc;
+    }
+  }
+  if (!ensure_smem(chunk_kernel<DH, true>, smem)) return RATP_ERR_CUDA;
+  chunk_kernel<DH, true><<<(unsigned)(pairs * pl.n_seg), kThreads, smem, st>>>(tq, tk, tv, p);
+  return launch_status();
+}
+
 // ---- cache ------------------------------------------------------------------
 struct CacheLayout {
   long long rows_per_b;
@@ -969,6 +1078,63 @@ int ratp_dilated_attn_prefill_per_sample_ws(const void* q, const void* hk, const
   if ((long long)B * T * H == 0) return RATP_OK;
   return launch_attn_tc(q, hk, hv, o, B, T, H, D_per_sample, 0, W, head_mask, workspace,
                         static_cast<cudaStream_t>(stream));
+}
+
+int ratp_linear_attn_workspace_bytes(int B, int T, int H, int Dh, size_t* bytes) {
+  if (!bytes) return RATP_ERR_ARG;
+  LinearPlan pl;
+  const int rc = linear_plan(B, T, H, Dh, &pl);
+  if (rc) return rc;
+  *bytes = linear_ws_bytes(pl, B, H, Dh);
+  return RATP_OK;
+}
+
+int ratp_linear_attn_prefill(const void* q, const void* k, const void* v, const float* log_decay,
+                             const float* initial_state, float* final_state, void* o,
+                             int B, int T, int H, int Dh, float scale, int dtype,
+                             void* workspace, size_t workspace_bytes, void* stream) {
+  LinearPlan pl;
+  int rc = linear_plan(B, T, H, Dh, &pl);
+  if (rc) return rc;
+  if ((long long)B * T * H == 0) return RATP_OK;
+  rc = check_linear(q, k, v, log_decay, initial_state, final_state, o, scale, dtype);
+  if (rc) return rc;
+  cudaStream_t st = static_cast<cudaStream_t>(stream);
+  if (T <= linear_attn::kRecurrentTokens)
+    return launch_linear_recurrent(q, k, v, log_decay, initial_state, final_state, o, B, T, H, Dh, scale, st);
+  const size_t need = linear_ws_bytes(pl, B, H, Dh);
+  if (need > 0) {
+    if (!workspace) return RATP_ERR_ARG;
+    if (!aligned16(workspace)) return RATP_ERR_ALIGN;
+    if (workspace_bytes < need) return RATP_ERR_CAPACITY;
+  }
+  linear_attn::Params p;
+  memset(&p, 0, sizeof(p));
+  p.o = static_cast<__nv_bfloat16*>(o);
+  p.log_decay = log_decay;
+  p.init = initial_state;
+  p.fin = final_state;
+  p.ws = static_cast<float*>(workspace);
+  p.B = B; p.T = T; p.H = H;
+  p.n_chunks = pl.n_chunks; p.seg_chunks = pl.seg_chunks; p.n_seg = pl.n_seg;
+  p.scale = scale;
+  p.o_align32 = (reinterpret_cast<uintptr_t>(o) & 31u) == 0;
+  CUtensorMap tq, tk, tv;
+  if (!make_chunk_map(&tq, q, B, T, H, Dh) || !make_chunk_map(&tk, k, B, T, H, Dh) || !make_chunk_map(&tv, v, B, T, H, Dh))
+    return RATP_ERR_CUDA;
+  return Dh == 128 ? launch_linear_chunks<128>(pl, tq, tk, tv, p, st) : launch_linear_chunks<64>(pl, tq, tk, tv, p, st);
+}
+
+int ratp_linear_attn_step(const void* q, const void* k, const void* v, const float* log_decay,
+                          float* state, void* o, int B, int H, int Dh, float scale, int dtype, void* stream) {
+  if (B < 0 || H < 0) return RATP_ERR_ARG;
+  if (Dh != 64 && Dh != 128) return RATP_ERR_SHAPE;
+  if ((long long)B * H == 0) return RATP_OK;
+  if (!state) return RATP_ERR_ARG;
+  const int rc = check_linear(q, k, v, log_decay, state, state, o, scale, dtype);
+  if (rc) return rc;
+  return launch_linear_recurrent(q, k, v, log_decay, state, state, o, B, 1, H, Dh, scale,
+                                 static_cast<cudaStream_t>(stream));
 }
 
 int ratp_qk_norm_rope(const ratp_view* q, const ratp_view* k, const ratp_view* q_out, const ratp_view* k_out,
