@@ -11,33 +11,38 @@
 //   all its time.
 // * chunk_kernel takes 128 tokens at a time on the tensor cores.  With S the
 //   state before the chunk, n the tokens in it, i, j = 0 .. n-1:
-//     o_i  = scale (a^{i+1} q_i S + sum_{j <= i} a^{i-j} (q_i . k_j) v_j)
+//     o_i  = scale a^{i+1} q_i S + sum_{j <= i} scale a^{i-j} (q_i . k_j) v_j
 //     S'   = a^n S + sum_j a^{n-1-j} k_j v_j^T
-//   that is, with P = mask(Q K^T) * a^{i-j}: two products read against the
+//   that is, with P = mask(Q K^T) * scale a^{i-j}: two products read against the
 //   chunk's values and state, and one that advances the state.
 //   No power of a is ever inverted, so any decay in (0, 1] is as exact as any
 //   other.  P and the state enter their products rounded to bf16 (as the
 //   attention's P does: the output is bf16 itself).  The state's own update
-//   keeps 16 bits of a^{n-1-j} k_j as two bf16 terms (hi + lo, two products),
+//   keeps all 24 bits of a^{n-1-j} k_j as three bf16 terms (three products),
 //   the products accumulate one chunk only, and the running state is fp32 in
-//   registers, so the state that is handed on is exact to fp32's order.
+//   registers, so the state that is handed on is as good as fp32 sums (two
+//   terms, 16 bits, left it 10 times further off than the plain fp32 form).
 //
 // A sequence is a chain over its chunks, so few (b, h) leave SMs idle: then
 // the chunks are cut into segments.  chunk_kernel<DH, false> computes every
 // segment's own state (from zero), combine_kernel turns those into the state
 // before each segment, and chunk_kernel<DH, true> runs all segments at once.
 //
-// Roles of chunk_kernel (320 threads, one CTA per SM):
-//   warps 0-3  P: read Q K^T from TMEM, mask, decay, write bf16 P to TMEM over
-//              it; then o = scale (a^{i+1} O1 + O2) out of TMEM to memory;
-//   warps 4-7  state: scale K in place to its hi part, lo part beside it; then
-//              S = a^n S + (TMEM) in registers, and S as bf16 in shared memory;
-//   warp 8     TMA producer: K, Q, V tiles through a ring of kSlots tiles;
-//   warp 9     TMEM and the MMA issuer.  Per chunk: P = Q K^T (M 128 tokens, N
-//              128 tokens), O1 = Q S, SL = K'^T V (M = Dh, hi then lo), O2 = P V.
-//   Without an output (<DH, false>) only SL is computed, and warps 0-3 share
-//   the scaling of K.
-// Bound: 4 tiles of memory traffic per chunk and (b, h) against five products.
+// Roles of chunk_kernel (448 threads, one CTA per SM):
+//   warps 0-3   P: read Q K^T from TMEM, mask, decay, write bf16 P to TMEM over
+//               it; then o = scale a^{i+1} O1 + O2 out of TMEM to memory;
+//   warps 4-11  state, half of its columns to each four warps: scale K in place
+//               to the first term, the others beside it, 32 tokens at a time
+//               through two buffers; S = a^n S + (TMEM) in registers; S as bf16
+//               in shared memory;
+//   warp 12     TMA producer: Q, K, V tiles through a ring of kSlots tiles;
+//   warp 13     TMEM and the MMA issuer: P = Q K^T (M 128 tokens, N 128 tokens),
+//               O1 = Q S, O2 = P V, SL = K'^T V (M = Dh).  Q K^T of the next
+//               chunk goes between the first and the other parts of SL, so that
+//               P of the next chunk is worked out while this one's state is.
+//   Without an output (<DH, false>) only SL is computed, in two buffers, and
+//   warps 0-3 share the scaling of K.
+// Bound: 4 tiles of memory traffic per chunk and (b, h) against six products.
 #pragma once
 #include "sm100.cuh"
 
@@ -45,10 +50,13 @@ namespace ratp {
 namespace linear_attn {
 
 constexpr int C = 128;                 // tokens per chunk
-constexpr int kThreads = 320;
-constexpr int kProducerWarp = 8;
-constexpr int kMmaWarp = 9;
+constexpr int kThreads = 448;
+constexpr int kStateWarps = 8;         // warps 4 .. 11
+constexpr int kProducerWarp = 12;
+constexpr int kMmaWarp = 13;
 constexpr int kSlots = 5;
+constexpr int kPart = 32;               // tokens whose scaled K is handed to the MMA at a time
+constexpr int kParts = C / kPart;
 constexpr int kRecurrentTokens = 16;
 
 // a^n for n >= 0 tokens.  log_decay is clamped to a finite value, below which
@@ -61,12 +69,15 @@ template <int DH>
 struct Layout {
   static constexpr uint32_t kHalf = C * 128;             // 128 rows x 64 bf16
   static constexpr uint32_t kTile = (DH / 64) * kHalf;
-  static constexpr uint32_t kOffLo = kSlots * kTile;     // K's lo part
-  static constexpr uint32_t kOffS = kOffLo + kTile;      // S, bf16 [DH / 64][DH rows][64]
+  static constexpr uint32_t kPartHalf = kPart * 128;     // 32 rows x 64 bf16
+  static constexpr uint32_t kPartTile = (DH / 64) * kPartHalf;
+  // second and third term of the scaled K: two buffers of two tiles of 32 rows
+  static constexpr uint32_t kOffLo = kSlots * kTile;
+  static constexpr uint32_t kOffS = kOffLo + 4 * kPartTile;  // S, bf16 [DH / 64][DH rows][64]
   static constexpr uint32_t kSHalf = DH * 128;
   static constexpr uint32_t kOffPow = kOffS + (DH / 64) * kSHalf;    // a^0 .. a^128
   static constexpr uint32_t kOffBar = kOffPow + (C + 1) * 4 + 4;
-  static constexpr int kBars = 2 * kSlots + 8;
+  static constexpr int kBars = 2 * kSlots + 14;
   static constexpr uint32_t kOffCtl = kOffBar + kBars * 8;           // TMEM address, abort flag
   // one CTA per SM whatever DH, since each takes all of TMEM
   static constexpr uint32_t kBytes = (kOffCtl + 8 + 1024) > 120 * 1024 ? (kOffCtl + 8 + 1024) : 120 * 1024;
@@ -88,13 +99,15 @@ struct Params {
   int o_align32;
 };
 
-// Two floats as bf16 pairs: hi the rounded values, lo what they leave.
-__device__ __forceinline__ void split2(float2 x, float2 w, uint32_t* hi, uint32_t* lo) {
+// x * w of two floats as three bf16 terms each: every term is what the ones
+// before leave, which fp32 holds exactly (x has 8 bits, w 24).
+__device__ __forceinline__ void split3(float2 x, float2 w, uint32_t* t0, uint32_t* t1, uint32_t* t2) {
   const float2 y = mul2(x, w);
-  *hi = pack_bf16x2(y.x, y.y);
-  const float2 h = make_float2(__uint_as_float(*hi << 16), __uint_as_float(*hi & 0xffff0000u));
-  const float2 r = fma2(x, w, make_float2(-h.x, -h.y));
-  *lo = pack_bf16x2(r.x, r.y);
+  *t0 = pack_bf16x2(y.x, y.y);
+  float2 r = fma2(x, w, make_float2(-__uint_as_float(*t0 << 16), -__uint_as_float(*t0 & 0xffff0000u)));
+  *t1 = pack_bf16x2(r.x, r.y);
+  r = sub2(r, make_float2(__uint_as_float(*t1 << 16), __uint_as_float(*t1 & 0xffff0000u)));
+  *t2 = pack_bf16x2(r.x, r.y);
 }
 
 template <int DH, bool OUT>
@@ -104,7 +117,8 @@ chunk_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ C
   using namespace sm100;
   using L = Layout<DH>;
   constexpr int NH = DH / 64;                            // 64-channel halves
-  constexpr int kUnits = OUT ? 3 : 2;                    // tiles per chunk: K, (Q,) V
+  constexpr int kUnits = OUT ? 3 : 2;                    // tiles per chunk: (Q,) K, V
+  constexpr int kK = OUT ? 1 : 0;                        // K's place among them
   constexpr uint32_t kColO1 = 128, kColO2 = kColO1 + DH, kColS = kColO2 + DH;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
@@ -112,7 +126,14 @@ chunk_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ C
   const uint32_t bar0 = sb + L::kOffBar;
   const uint32_t b_full = bar0, b_empty = bar0 + 8 * kSlots;
   const uint32_t b_qk = bar0 + 8 * (2 * kSlots), b_p = b_qk + 8, b_o = b_qk + 16, b_ofree = b_qk + 24;
-  const uint32_t b_kp = b_qk + 32, b_kv = b_qk + 40, b_s = b_qk + 48, b_final = b_qk + 56;
+  // part g = kParts c + part of this CTA's tokens uses buffer g & 1, and these
+  // barriers' phase g / 2
+  const uint32_t b_kp = b_qk + 32;                       // [2]: part scaled
+  const uint32_t b_kv = b_qk + 48;                       // [2]: its products done
+  const uint32_t b_s = b_qk + 64, b_final = b_qk + 72;
+  // chunk c's state products done, and (<DH, false>) their TMEM buffer read:
+  // barriers [c & 1], phase c / 2
+  const uint32_t b_pd = b_qk + 80, b_sf = b_qk + 96;
   float* s_pow = reinterpret_cast<float*>(smem + L::kOffPow);
   uint32_t* s_tmem = reinterpret_cast<uint32_t*>(smem + L::kOffCtl);
   volatile int* s_abort = reinterpret_cast<volatile int*>(smem + L::kOffCtl + 4);
@@ -141,9 +162,13 @@ chunk_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ C
     mbar_init(b_p, 128);
     mbar_init(b_o, 1);
     mbar_init(b_ofree, 128);
-    mbar_init(b_kp, OUT ? 128 : 256);
-    mbar_init(b_kv, 1);
-    mbar_init(b_s, 128);
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(b_kp + 8 * i, 128);
+      mbar_init(b_kv + 8 * i, 1);
+      mbar_init(b_pd + 8 * i, 1);
+      mbar_init(b_sf + 8 * i, 32 * kStateWarps);
+    }
+    mbar_init(b_s, 32 * kStateWarps);
     mbar_init(b_final, 1);
     fence_barrier_init();
   }
@@ -158,33 +183,47 @@ chunk_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ C
   tc_fence_after();
   const uint32_t tmem = *s_tmem;
 
-  // tile u of this CTA (chunk u / kUnits; K, (Q,) V in turn) lies in slot u % kSlots
+  // tile u of this CTA (chunk u / kUnits; (Q,) K, V in turn) lies in slot u % kSlots
   auto full_wait = [&](int u) { return mbar_wait(b_full + 8 * (u % kSlots), (uint32_t)(u / kSlots) & 1u, s_abort); };
   auto tile = [&](int u) { return sb + (uint32_t)(u % kSlots) * L::kTile; };
 
-  // a^{n-1-j} k_j of chunk c, hi in place and lo beside it, by threads
-  // tid + part * 128 of parts * 128; zero rows past the sequence stay zero
-  auto scale_k = [&](int c, int tid, int part, int parts) {
+  auto kv_wait = [&](int g) { return mbar_wait(b_kv + 8 * (g & 1), (uint32_t)(g >> 1) & 1u, s_abort); };
+  // a^{n-1-j} k_j for parts first, first + step, .. of chunk c by one group of
+  // 128 threads: the first term in place, the others into the part's buffer
+  // (free once the products of the part that used it are done); zero rows past
+  // the sequence stay zero.  A part is a chain of latencies (the buffer, the
+  // loads, the stores' fence), so two groups work on two parts at a time.
+  auto scale_k = [&](int c, int tid, int first, int step) -> bool {
     const int m = tokens(c);
-    uint8_t* t = smem + (uint32_t)((c * kUnits) % kSlots) * L::kTile;
-    uint8_t* lo = smem + L::kOffLo;
-#pragma unroll 4
-    for (int i = part; i < NH * 8; i += parts) {
-      const int row = (i & 7) * 16 + tid / 8;            // 16 bytes of row `row`, half i / 8 (swizzled within it)
-      const uint32_t off = (uint32_t)(i * 128 + tid) * 16;
-      const float w = s_pow[max(m - 1 - row, 0)];
-      const float2 w2 = make_float2(w, w);
-      float2 f[4];
-      Elem<__nv_bfloat16>::unpack2(*reinterpret_cast<const uint4*>(t + off), f);
-      uint4 hv, lv;
-      split2(f[0], w2, &hv.x, &lv.x);
-      split2(f[1], w2, &hv.y, &lv.y);
-      split2(f[2], w2, &hv.z, &lv.z);
-      split2(f[3], w2, &hv.w, &lv.w);
-      *reinterpret_cast<uint4*>(t + off) = hv;
-      *reinterpret_cast<uint4*>(lo + off) = lv;
+    uint8_t* t = smem + (uint32_t)((c * kUnits + kK) % kSlots) * L::kTile;
+#pragma unroll 1
+    for (int part = first; part < kParts; part += step) {
+      const int g = c * kParts + part;
+      if (g >= 2 && !warp_all(kv_wait(g - 2))) return false;
+      uint8_t* lo = smem + L::kOffLo + (uint32_t)(g & 1) * 2 * L::kPartTile;
+#pragma unroll
+      for (int it = 0; it < NH * kPart * 8 / 128; ++it) {
+        const int i = tid + it * 128;
+        const int hf = i / (kPart * 8), in = i % (kPart * 8);   // 16 bytes of row in / 8 (swizzled within it)
+        uint4* src = reinterpret_cast<uint4*>(t + hf * L::kHalf + part * L::kPartHalf + in * 16);
+        uint4* dst = reinterpret_cast<uint4*>(lo + hf * L::kPartHalf + in * 16);
+        const float w = s_pow[max(m - 1 - part * kPart - in / 8, 0)];
+        const float2 w2 = make_float2(w, w);
+        float2 f[4];
+        Elem<__nv_bfloat16>::unpack2(*src, f);
+        uint4 v0, v1, v2;
+        split3(f[0], w2, &v0.x, &v1.x, &v2.x);
+        split3(f[1], w2, &v0.y, &v1.y, &v2.y);
+        split3(f[2], w2, &v0.z, &v1.z, &v2.z);
+        split3(f[3], w2, &v0.w, &v1.w, &v2.w);
+        *src = v0;
+        *dst = v1;
+        *reinterpret_cast<uint4*>(reinterpret_cast<uint8_t*>(dst) + L::kPartTile) = v2;
+      }
+      asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+      mbar_arrive(b_kp + 8 * (g & 1));
     }
-    asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+    return true;
   };
 
   if (warp == kProducerWarp) {
@@ -199,7 +238,7 @@ chunk_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ C
         const int t0 = (c0 + c) * C;
 #pragma unroll
         for (int i = 0; i < kUnits; ++i, ++u) {
-          const CUtensorMap* m = i == 0 ? &tm_k : i == kUnits - 1 ? &tm_v : &tm_q;
+          const CUtensorMap* m = i == kK ? &tm_k : i == kK + 1 ? &tm_v : &tm_q;
           if (u >= kSlots && !mbar_wait(b_empty + 8 * (u % kSlots), (uint32_t)(u / kSlots - 1) & 1u, s_abort)) {
             ok = false;
             break;
@@ -221,50 +260,36 @@ chunk_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ C
       constexpr uint32_t idO1 = idesc_bf16_f32(C, DH, 0, 1);     // Q S: S is [dk][dv], N-major
       constexpr uint32_t idO2 = idesc_bf16_f32(C, DH, 0, 1);     // P V: P in TMEM
       constexpr uint32_t idS = idesc_bf16_f32(128, DH, 1, 1);    // K'^T V: K' is [token][dk], M-major
-      // M is 128 for DH = 64 too: both halves of M read the same 64 channels,
-      // and lanes 64..127 of the result are not used
-      constexpr uint32_t kMHalf = DH == 128 ? L::kHalf : 0;
       bool ok = true;
-      for (int c = 0; c < n && ok; ++c) {
-        const int uk = c * kUnits, uv = uk + kUnits - 1;
-        const uint32_t par = (uint32_t)c & 1u;
-        if (OUT) {
-          const int uq = uk + 1;
-          if (!full_wait(uk) || !full_wait(uq)) { ok = false; break; }
-          tc_fence_after();
-          const uint64_t dq = sw128_desc(tile(uq), 16, 1024), dk = sw128_desc(tile(uk), 16, 1024);
+      auto issue_qk = [&](int c) -> bool {
+        const int uq = c * kUnits, uk = uq + 1;
+        if (!full_wait(uq) || !full_wait(uk)) return false;
+        tc_fence_after();
+        const uint64_t dq = sw128_desc(tile(uq), 16, 1024), dk = sw128_desc(tile(uk), 16, 1024);
 #pragma unroll
-          for (int k = 0; k < DH / 16; ++k) {
-            const uint64_t off = (uint64_t)(((k >> 2) * L::kHalf + (k & 3) * 32) >> 4);
-            umma_f16(tmem + kColP, dq + off, dk + off, idP, k > 0 ? 1u : 0u);
-          }
-          umma_commit(b_qk);
+        for (int k = 0; k < DH / 16; ++k) {
+          const uint64_t off = (uint64_t)(((k >> 2) * L::kHalf + (k & 3) * 32) >> 4);
+          umma_f16(tmem + kColP, dq + off, dk + off, idP, k > 0 ? 1u : 0u);
+        }
+        umma_commit(b_qk);
+        return true;
+      };
+      if (OUT && !issue_qk(0)) ok = false;
+      for (int c = 0; c < n && ok; ++c) {
+        const int uk = c * kUnits + kK, uv = uk + 1;
+        const uint32_t par = (uint32_t)c & 1u;
+        const uint64_t dv = sw128_desc(tile(uv), L::kHalf, 1024);
+        if (OUT) {
+          const int uq = uk - 1;
           if (!mbar_wait(b_s, par, s_abort) || (c > 0 && !mbar_wait(b_ofree, par ^ 1u, s_abort))) { ok = false; break; }
           tc_fence_after();
-          const uint64_t ds = sw128_desc(sb + L::kOffS, L::kSHalf, 1024);
+          const uint64_t dq = sw128_desc(tile(uq), 16, 1024), ds = sw128_desc(sb + L::kOffS, L::kSHalf, 1024);
 #pragma unroll
           for (int k = 0; k < DH / 16; ++k) {
             const uint64_t off = (uint64_t)(((k >> 2) * L::kHalf + (k & 3) * 32) >> 4);
             umma_f16(tmem + kColO1, dq + off, ds + (uint64_t)((k * 16 * 128) >> 4), idO1, k > 0 ? 1u : 0u);
           }
           umma_commit(b_empty + 8 * (uq % kSlots));
-        }
-        const uint64_t dv = sw128_desc(tile(uv), L::kHalf, 1024);
-        if (c < n_state) {
-          if (!mbar_wait(b_kp, par, s_abort) || !full_wait(uv)) { ok = false; break; }
-          tc_fence_after();
-#pragma unroll
-          for (int part = 0; part < 2; ++part) {
-            const uint64_t da = sw128_desc(part == 0 ? tile(uk) : sb + L::kOffLo, kMHalf, 1024);
-#pragma unroll
-            for (int k = 0; k < C / 16; ++k)
-              umma_f16(tmem + kColS, da + (uint64_t)((k * 16 * 128) >> 4), dv + (uint64_t)((k * 16 * 128) >> 4), idS,
-                       part + k > 0 ? 1u : 0u);
-          }
-          umma_commit(b_kv);
-        }
-        umma_commit(b_empty + 8 * (uk % kSlots));
-        if (OUT) {
           if (!mbar_wait(b_p, par, s_abort) || !full_wait(uv)) { ok = false; break; }
           tc_fence_after();
 #pragma unroll
@@ -272,6 +297,36 @@ chunk_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ C
             umma_f16_ts(tmem + kColO2, tmem + kColP + k * 8, dv + (uint64_t)((k * 16 * 128) >> 4), idO2, k > 0 ? 1u : 0u);
           umma_commit(b_o);
         }
+        const uint32_t tS = tmem + (OUT ? kColS : (uint32_t)(c & 1) * 128u);
+        if (!OUT && (!full_wait(uv) || (c >= 2 && !mbar_wait(b_sf + 8 * (c & 1), (uint32_t)((c >> 1) - 1) & 1u, s_abort)))) {
+          ok = false;
+          break;
+        }
+#pragma unroll 1
+        for (int part = 0; part < kParts; ++part) {
+          if (OUT && part == 1 && c + 1 < n && !issue_qk(c + 1)) { ok = false; break; }
+          if (c >= n_state) continue;
+          const int g = c * kParts + part;
+          if (!mbar_wait(b_kp + 8 * (g & 1), (uint32_t)(g >> 1) & 1u, s_abort)) { ok = false; break; }
+          tc_fence_after();
+          const uint32_t lo = sb + L::kOffLo + (uint32_t)(g & 1) * 2 * L::kPartTile;
+          const uint64_t db = dv + (uint64_t)(part * L::kPartHalf >> 4);
+#pragma unroll
+          for (int term = 0; term < 3; ++term) {
+            // K' is [token][dk]; M is 128 for DH = 64 too: both halves of M read
+            // the same 64 channels, and lanes 64..127 of the result are not used
+            const uint64_t da = term == 0 ? sw128_desc(tile(uk) + part * L::kPartHalf, DH == 128 ? L::kHalf : 0, 1024)
+                                          : sw128_desc(lo + (term - 1) * L::kPartTile, DH == 128 ? L::kPartHalf : 0, 1024);
+#pragma unroll
+            for (int k = 0; k < kPart / 16; ++k)
+              umma_f16(tS, da + (uint64_t)((k * 16 * 128) >> 4), db + (uint64_t)((k * 16 * 128) >> 4), idS,
+                       part + term + k > 0 ? 1u : 0u);
+          }
+          umma_commit(b_kv + 8 * (g & 1));
+        }
+        if (!ok) break;
+        if (c < n_state) umma_commit(b_pd + 8 * (c & 1));
+        umma_commit(b_empty + 8 * (uk % kSlots));
         umma_commit(b_empty + 8 * (uv % kSlots));
       }
       umma_commit(b_final);                              // all MMAs done before TMEM is released
@@ -283,13 +338,21 @@ chunk_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ C
     if (OUT) {
       // ---------------------------------------------------------- P and o
       const int i = warp * 32 + lane;                    // token row of the chunk (TMEM lane)
+      // The powers each thread needs are the same for every chunk and sit in
+      // registers: the products read shared memory at its full rate, and a
+      // load from it waits long.  Before the diagonal a^{i - j} =
+      // a^{i - 32q - 31} a^{31 - jj}; on it, 2^(log2(a) (i - j)) at P's bf16
+      // precision.
       const float ai = s_pow[i + 1] * p.scale;
+      const float l2a = fmaxf(ld, -1.0e4f) * 1.4426950408889634f;
+      float row[3];
+#pragma unroll
+      for (int q = 0; q < 3; ++q) row[q] = s_pow[max(i - 32 * q - 31, 0)] * p.scale;
       float2 col[16];                                    // a^{31 - jj}, the same for every lane
 #pragma unroll
       for (int x = 0; x < 16; ++x) col[x] = make_float2(s_pow[31 - 2 * x], s_pow[30 - 2 * x]);
-      for (int c = 0; c < n; ++c) {
-        const uint32_t par = (uint32_t)c & 1u;
-        if (!warp_all(mbar_wait(b_qk, par, s_abort))) break;
+      auto work_p = [&](int c) -> bool {
+        if (!warp_all(mbar_wait(b_qk, (uint32_t)c & 1u, s_abort))) return false;
         tc_fence_after();
 #pragma unroll
         for (int q = 0; q < 4; ++q) {                    // columns 32 q .. 32 q + 31
@@ -299,20 +362,19 @@ chunk_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ C
             tmem_ld32(tl + kColP + 32 * q, r);
             tmem_wait_ld();
             if (q < warp) {
-              const float f = s_pow[i - 32 * q - 31];    // a^{i - j} = a^{i - 32q - 31} a^{31 - jj}
-              const float2 f2 = make_float2(f, f);
+              const float2 f2 = make_float2(row[q < 3 ? q : 0], row[q < 3 ? q : 0]);
 #pragma unroll
               for (int x = 0; x < 16; ++x) {
-                const float2 y = mul2(make_float2(__uint_as_float(r[2 * x]), __uint_as_float(r[2 * x + 1])), mul2(f2, col[x]));
+                const float2 y = mul2(mul2(make_float2(__uint_as_float(r[2 * x]), __uint_as_float(r[2 * x + 1])), f2), col[x]);
                 w[x] = pack_bf16x2(y.x, y.y);
               }
             } else {
 #pragma unroll
-              for (int x = 0; x < 16; ++x) {
+              for (int x = 0; x < 16; ++x) {             // branch-free: a masked value is cut off by its bits
                 const int d0 = lane - 2 * x, d1 = d0 - 1;
-                const float y0 = d0 >= 0 ? __uint_as_float(r[2 * x]) * s_pow[max(d0, 0)] : 0.f;
-                const float y1 = d1 >= 0 ? __uint_as_float(r[2 * x + 1]) * s_pow[max(d1, 0)] : 0.f;
-                w[x] = pack_bf16x2(y0, y1);
+                const float y0 = __uint_as_float(r[2 * x]) * (p.scale * exp2f(l2a * (float)max(d0, 0)));
+                const float y1 = __uint_as_float(r[2 * x + 1]) * (p.scale * exp2f(l2a * (float)max(d1, 0)));
+                w[x] = pack_bf16x2(y0, y1) & ~((uint32_t)(d0 >> 31) & 0xffffu) & ~((uint32_t)(d1 >> 31) & 0xffff0000u);
               }
             }
           } else {
@@ -324,73 +386,80 @@ chunk_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ C
         tmem_wait_st();
         tc_fence_before();
         mbar_arrive(b_p);
-        if (!warp_all(mbar_wait(b_o, par, s_abort))) break;
+        return true;
+      };
+      auto work_o = [&](int c) -> bool {
+        if (!warp_all(mbar_wait(b_o, (uint32_t)c & 1u, s_abort))) return false;
         tc_fence_after();
         const int t = (c0 + c) * C + i;
         __nv_bfloat16* orow = p.o + (((size_t)b * p.T + t) * p.H + h) * DH;
         const bool there = t < p.T && RATP_IN((((long long)b * p.T + t) * p.H + h) * DH, DH, (long long)p.B * p.T * p.H * DH);
+        const float2 a2 = make_float2(ai, ai);
 #pragma unroll 1
         for (int q = 0; q < DH / 32; ++q) {
           uint32_t r1[32], r2[32];
           tmem_ld32(tl + kColO1 + 32 * q, r1);
           tmem_ld32(tl + kColO2 + 32 * q, r2);
           tmem_wait_ld();
+          uint32_t y[16];
+#pragma unroll
+          for (int x = 0; x < 16; ++x) {
+            const float2 v = fma2(a2, make_float2(__uint_as_float(r1[2 * x]), __uint_as_float(r1[2 * x + 1])),
+                                  make_float2(__uint_as_float(r2[2 * x]), __uint_as_float(r2[2 * x + 1])));
+            y[x] = pack_bf16x2(v.x, v.y);
+          }
           if (there) {
+            __nv_bfloat16* dst = orow + 32 * q;
+            if (p.o_align32) {
 #pragma unroll
-            for (int v = 0; v < 2; ++v) {
-              uint32_t y[8];
-#pragma unroll
-              for (int x = 0; x < 8; ++x) {
-                const int e = 16 * v + 2 * x;
-                y[x] = pack_bf16x2(fmaf(ai, __uint_as_float(r1[e]), p.scale * __uint_as_float(r2[e])),
-                                   fmaf(ai, __uint_as_float(r1[e + 1]), p.scale * __uint_as_float(r2[e + 1])));
-              }
-              __nv_bfloat16* dst = orow + 32 * q + 16 * v;
-              if (p.o_align32) {
+              for (int v = 0; v < 16; v += 8)
                 asm volatile("st.global.v8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};"
-                             :: "l"(dst), "r"(y[0]), "r"(y[1]), "r"(y[2]), "r"(y[3]), "r"(y[4]), "r"(y[5]), "r"(y[6]), "r"(y[7])
-                             : "memory");
-              } else {
-                *reinterpret_cast<uint4*>(dst) = make_uint4(y[0], y[1], y[2], y[3]);
-                *reinterpret_cast<uint4*>(dst + 8) = make_uint4(y[4], y[5], y[6], y[7]);
-              }
+                             :: "l"(dst + 2 * v), "r"(y[v]), "r"(y[v + 1]), "r"(y[v + 2]), "r"(y[v + 3]), "r"(y[v + 4]),
+                                "r"(y[v + 5]), "r"(y[v + 6]), "r"(y[v + 7]) : "memory");
+            } else {
+#pragma unroll
+              for (int v = 0; v < 16; v += 4)
+                *reinterpret_cast<uint4*>(dst + 2 * v) = make_uint4(y[v], y[v + 1], y[v + 2], y[v + 3]);
             }
           }
         }
         tc_fence_before();
         mbar_arrive(b_ofree);
-      }
+        return true;
+      };
+      // P of the next chunk before this one's output: its products come first
+      bool ok = work_p(0);
+      for (int c = 0; c < n && ok; ++c) ok = (c + 1 >= n || work_p(c + 1)) && work_o(c);
     } else {
-      for (int c = 0; c < n; ++c) {
-        // K's tile is there, and lo was read by the chunk before
-        if (!warp_all(full_wait(c * kUnits) && (c == 0 || mbar_wait(b_kv, (uint32_t)(c - 1) & 1u, s_abort)))) break;
-        scale_k(c, threadIdx.x, 0, 2);
-        mbar_arrive(b_kp);
-      }
+      // parts 0 and 2; the state warps' second half has 1 and 3
+      for (int c = 0; c < n; ++c)
+        if (!warp_all(full_wait(c * kUnits + kK)) || !scale_k(c, threadIdx.x, 0, 2)) break;
     }
   } else {
     // ------------------------------------------------------------ state
-    const int tid = threadIdx.x - 128, sw = warp - 4;
-    const int r = sw * 32 + lane;                        // row of S (TMEM lane)
+    constexpr int NC = DH / 2;                           // columns of S per thread
+    const int tid = threadIdx.x - 128, col0 = tid / 128 * NC;
+    const int r = (warp & 3) * 32 + lane;                // row of S (TMEM lane)
     const bool mine = r < DH;                            // whole warps: DH is 64 or 128
-    const uint32_t tl = tmem + ((uint32_t)(sw * 32) << 16) + kColS;
-    float S[DH];
+    const uint32_t tl = tmem + ((uint32_t)((warp & 3) * 32) << 16) + col0;
+    float S[NC];
     const float* src = nullptr;                          // the state before this segment
     if (OUT) src = p.n_seg > 1 ? p.ws + ((size_t)pair * p.n_seg + seg) * DH * DH
                                : p.init != nullptr ? p.init + (size_t)pair * DH * DH : nullptr;
     [[maybe_unused]] const long long n_src = (long long)p.B * p.H * p.n_seg * DH * DH;
-    const bool load = mine && src != nullptr && RATP_IN(((long long)pair * p.n_seg + (p.n_seg > 1 ? seg : 0)) * DH * DH + r * DH, DH, n_src);
+    const long long at = (long long)r * DH + col0;
+    const bool load = mine && src != nullptr && RATP_IN(((long long)pair * p.n_seg + seg) * DH * DH + at, NC, n_src);
 #pragma unroll
-    for (int x = 0; x < DH; x += 4) {
-      const float4 v = load ? *reinterpret_cast<const float4*>(src + r * DH + x) : make_float4(0.f, 0.f, 0.f, 0.f);
+    for (int x = 0; x < NC; x += 4) {
+      const float4 v = load ? *reinterpret_cast<const float4*>(src + at + x) : make_float4(0.f, 0.f, 0.f, 0.f);
       S[x] = v.x; S[x + 1] = v.y; S[x + 2] = v.z; S[x + 3] = v.w;
     }
     auto publish = [&]() {                               // S as bf16, [half][row][64], 128-byte swizzle
       if (mine) {
 #pragma unroll
-        for (int x = 0; x < DH; x += 8) {
-          const int ch = (x & 63) / 8;
-          *reinterpret_cast<uint4*>(smem + L::kOffS + (x / 64) * L::kSHalf + r * 128 + ((ch ^ (r & 7)) * 16)) =
+        for (int x = 0; x < NC; x += 8) {
+          const int cc = col0 + x, ch = (cc & 63) / 8;
+          *reinterpret_cast<uint4*>(smem + L::kOffS + (cc / 64) * L::kSHalf + r * 128 + ((ch ^ (r & 7)) * 16)) =
               make_uint4(pack_bf16x2(S[x], S[x + 1]), pack_bf16x2(S[x + 2], S[x + 3]), pack_bf16x2(S[x + 4], S[x + 5]),
                          pack_bf16x2(S[x + 6], S[x + 7]));
         }
@@ -398,36 +467,57 @@ chunk_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ C
       asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
       mbar_arrive(b_s);
     };
-    if (OUT) publish();
-    bool ok = true;
-    for (int c = 0; c < n_state; ++c) {
-      const uint32_t par = (uint32_t)c & 1u;
-      // K's tile is there; Q K^T has read it; lo was read before the last update
-      if (!warp_all(full_wait(c * kUnits) && (!OUT || mbar_wait(b_qk, par, s_abort)))) { ok = false; break; }
-      scale_k(c, tid, OUT ? 0 : 1, OUT ? 1 : 2);
-      tc_fence_before();
-      mbar_arrive(b_kp);
-      if (!warp_all(mbar_wait(b_kv, par, s_abort))) { ok = false; break; }
+    // S = a^n S + chunk c's products, which are done
+    auto update = [&](int c) {
       tc_fence_after();
       const float a = s_pow[tokens(c)];
+      const uint32_t tc = tl + (OUT ? kColS : (uint32_t)(c & 1) * 128u);
       if (mine) {
 #pragma unroll
-        for (int q = 0; q < DH / 32; ++q) {
+        for (int q = 0; q < NC / 32; ++q) {
           uint32_t v[32];
-          tmem_ld32(tl + 32 * q, v);
+          tmem_ld32(tc + 32 * q, v);
           tmem_wait_ld();
 #pragma unroll
           for (int x = 0; x < 32; ++x) S[32 * q + x] = fmaf(a, S[32 * q + x], __uint_as_float(v[x]));
         }
       }
-      if (OUT && c + 1 < n) publish();
+      tc_fence_before();
+    };
+    auto products = [&](int c) { return warp_all(mbar_wait(b_pd + 8 * (c & 1), (uint32_t)(c >> 1) & 1u, s_abort)); };
+    bool ok = true;
+    if (OUT) {
+      publish();
+      for (int c = 0; c < n_state; ++c) {
+        // K's tile is there, and Q K^T has read it
+        if (!warp_all(full_wait(c * kUnits + kK) && mbar_wait(b_qk, (uint32_t)c & 1u, s_abort)) || !scale_k(c, tid & 127, tid / 128, 2) ||
+            !products(c)) {
+          ok = false;
+          break;
+        }
+        update(c);
+        if (c + 1 < n) publish();
+      }
+    } else {
+      // the second half's scaling runs one chunk ahead of its update
+      for (int c = 0; c <= n; ++c) {
+        if ((tid >= 128 && c < n && (!warp_all(full_wait(c * kUnits + kK)) || !scale_k(c, tid & 127, 1, 2))) ||
+            (c > 0 && !products(c - 1))) {
+          ok = false;
+          break;
+        }
+        if (c > 0) {
+          update(c - 1);
+          mbar_arrive(b_sf + 8 * ((c - 1) & 1));
+        }
+      }
     }
     float* dst = OUT ? (want_end ? p.fin + (size_t)pair * DH * DH : nullptr)
                      : p.ws + ((size_t)pair * p.n_seg + seg) * DH * DH;
     if (ok && mine && dst != nullptr) {
 #pragma unroll
-      for (int x = 0; x < DH; x += 4)
-        *reinterpret_cast<float4*>(dst + r * DH + x) = make_float4(S[x], S[x + 1], S[x + 2], S[x + 3]);
+      for (int x = 0; x < NC; x += 4)
+        *reinterpret_cast<float4*>(dst + at + x) = make_float4(S[x], S[x + 1], S[x + 2], S[x + 3]);
     }
   }
 
@@ -451,13 +541,21 @@ combine_kernel(float* __restrict__ ws, const float* __restrict__ init, const flo
   if (!RATP_IN(((long long)pair * n_seg * quads + e) * 4, ((long long)(n_seg - 1) * quads + 1) * 4, n_ws)) return;
   float4 run = init != nullptr ? reinterpret_cast<const float4*>(init)[(long long)pair * quads + e]
                                : make_float4(0.f, 0.f, 0.f, 0.f);
-  for (int s = 0; s < n_seg; ++s) {
-    const float4 own = s + 1 < n_seg ? w[(long long)s * quads] : make_float4(0.f, 0.f, 0.f, 0.f);
-    w[(long long)s * quads] = run;
-    run.x = fmaf(a, run.x, own.x);
-    run.y = fmaf(a, run.y, own.y);
-    run.z = fmaf(a, run.z, own.z);
-    run.w = fmaf(a, run.w, own.w);
+  constexpr int kBatch = 8;                              // segments whose loads are in flight at once
+  for (int s0 = 0; s0 < n_seg; s0 += kBatch) {
+    float4 own[kBatch];
+#pragma unroll
+    for (int i = 0; i < kBatch; ++i)
+      own[i] = s0 + i + 1 < n_seg ? w[(long long)(s0 + i) * quads] : make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+    for (int i = 0; i < kBatch; ++i) {
+      if (s0 + i >= n_seg) break;
+      w[(long long)(s0 + i) * quads] = run;
+      run.x = fmaf(a, run.x, own[i].x);
+      run.y = fmaf(a, run.y, own[i].y);
+      run.z = fmaf(a, run.z, own[i].z);
+      run.w = fmaf(a, run.w, own[i].w);
+    }
   }
 }
 
