@@ -6,8 +6,10 @@ stream.  There is no CPU fallback -- if the library is missing the calls raise.
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes
 import os
+import struct
 import threading
 
 import torch
@@ -57,13 +59,8 @@ class DecodeLayerStruct(ctypes.Structure):
     ]
 
 
-class ViewStruct(ctypes.Structure):
-    """Mirror of ``struct ratp_view``."""
-    _fields_ = [
-        ("data", ctypes.c_void_p),
-        ("stride_b", ctypes.c_int64), ("stride_t", ctypes.c_int64), ("stride_h", ctypes.c_int64),
-        ("heads", ctypes.c_int32),
-    ]
+# struct ratp_view {data, stride_b, stride_t, stride_h, heads}, as bytes
+_VIEW = struct.Struct("=QqqqiI")
 
 
 _lib = None
@@ -91,7 +88,7 @@ _SIGS = {
     "ratp_dilated_attn_prefill_per_sample_ws": ([_P, _P, _P, _P, _I, _I, _I, _I, _P, _I, _P, _I, _P, _P], _I),
     "ratp_prefill_fused_workspace_bytes": ([_I, _I, _I, _I, ctypes.POINTER(_SZ)], _I),
     "ratp_prefill_fused": ([_P, _P, _P, _P, _P, _P, _P, _P, _I, _I, _I, _I, _I, _I, _P, _I, _P, _SZ, _P], _I),
-    "ratp_qk_norm_rope": ([ctypes.POINTER(ViewStruct)] * 4 + [_P] * 4 + [_I] * 6 + [ctypes.c_float, _I, _P], _I),
+    "ratp_qk_norm_rope": ([ctypes.c_char_p] * 4 + [_P] * 4 + [_I] * 6 + [ctypes.c_float, _I, _P], _I),
     "ratp_linear_attn_workspace_bytes": ([_I, _I, _I, _I, ctypes.POINTER(_SZ)], _I),
     "ratp_linear_attn_prefill": ([_P] * 7 + [_I] * 4 + [ctypes.c_float, _I, _P, _SZ, _P], _I),
     "ratp_linear_attn_step": ([_P] * 6 + [_I] * 3 + [ctypes.c_float, _I, _P], _I),
@@ -113,6 +110,8 @@ _SIGS = {
 def load_library(path: str = LIB_PATH):
     """Load ``libratp.so``; raises if it has not been built."""
     global _lib
+    if _lib is not None:
+        return _lib
     with _lock:
         if _lib is None:
             if not os.path.exists(path):
@@ -137,26 +136,23 @@ def _check(fn, code):
         raise RatpError(fn, code)
 
 
+# handle of a device's current stream without a Stream object (2.4 -> 0.2 us)
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+
+
 def _stream(t: torch.Tensor):
-    return ctypes.c_void_p(torch.cuda.current_stream(t.device).cuda_stream)
+    if _raw_stream is not None:
+        return _raw_stream(t.get_device())
+    return torch.cuda.current_stream(t.device).cuda_stream
 
 
-class _on:
-    """Makes ``device`` current inside the block (nothing to do, and nothing
+_HERE = contextlib.nullcontext()
+
+
+def _on(index):
+    """Context with device ``index`` current (nothing to do, and next to nothing
     paid, where it is already)."""
-
-    def __init__(self, device):
-        self.index = device.index
-
-    def __enter__(self):
-        self.guard = None
-        if self.index is not None and self.index != torch.cuda.current_device():
-            self.guard = torch.cuda.device(self.index)
-            self.guard.__enter__()
-
-    def __exit__(self, *exc):
-        if self.guard is not None:
-            self.guard.__exit__(*exc)
+    return _HERE if index == torch.cuda.current_device() else torch.cuda.device(index)
 
 
 def _addr(t):
@@ -437,23 +433,36 @@ def prefill_fused(q, xk, xv, g, D, W=0, head_mask=None, hk=None, hv=None, out=No
     return out, hk, hv
 
 
-def _head_rows(t, name, dtype, device):
-    """(B, T, H, Dh, strides of b, t, h) of a [B, T, H, Dh] or [B, H, Dh] view
-    whose channels are contiguous."""
+def _head_view(t, name, dtype, device, shape=None):
+    """(shape, packed ratp_view) of a [B, T, H, Dh] or [B, H, Dh] view whose
+    channels are contiguous."""
     if not isinstance(t, torch.Tensor) or not t.is_cuda:
         raise ValueError("%s must be a CUDA tensor" % name)
-    if t.dtype != dtype or t.device != device:
-        raise ValueError("%s must be %s on %s, got %s on %s" % (name, dtype, device, t.dtype, t.device))
-    if t.dim() == 4:
-        (B, T, H, Dh), (sb, st, sh, sc) = t.shape, t.stride()
-    elif t.dim() == 3:
-        (B, H, Dh), (sb, sh, sc), T, st = t.shape, t.stride(), 1, 0
-    else:
+    if t.dtype != dtype or t.get_device() != device:
+        raise ValueError("%s must be %s on cuda:%d, got %s on %s" % (name, dtype, device, t.dtype, t.device))
+    sz, st = t.shape, t.stride()
+    n = len(sz)
+    if shape is not None and sz != shape:
+        raise ValueError("%s must have the shape %s" % (name, tuple(shape)))
+    if n != 4 and n != 3:
         raise ValueError("%s must be [B, T, H, Dh] or [B, H, Dh]" % name)
-    if sc != 1 and Dh > 1:
+    if st[-1] != 1 and sz[-1] > 1:
         raise ValueError("%s: channels must be contiguous" % name)
     # the stride of a dimension of one element is never used
-    return B, T, H, Dh, sb if B > 1 else 0, st if T > 1 else 0, sh if H > 1 else 0
+    H = sz[-2]
+    return sz, _VIEW.pack(t.data_ptr(), st[0] if sz[0] > 1 else 0, st[1] if n == 4 and sz[1] > 1 else 0,
+                          st[-2] if H > 1 else 0, H, 0)
+
+
+def _new_head_view(sz, dtype, device):
+    """A new dense tensor of shape ``sz`` and its packed ratp_view."""
+    t = torch.empty(sz, dtype=dtype, device=device)
+    H, Dh = sz[-2], sz[-1]
+    T = sz[1] if len(sz) == 4 else 1
+    return t, _VIEW.pack(t.data_ptr(), T * H * Dh, H * Dh, Dh, H, 0)
+
+
+_NO_VIEW = _VIEW.pack(0, 0, 0, 0, 0, 0)
 
 
 def qk_norm_rope(q, k, q_weight, k_weight, inv_freq, positions=None, eps=1e-6, interleaved=False,
@@ -474,56 +483,51 @@ def qk_norm_rope(q, k, q_weight, k_weight, inv_freq, positions=None, eps=1e-6, i
     first token here, e.g. ``KVCache.lengths()``) or int32 [B, T].
     q_out, k_out: outputs; q and k themselves work in place."""
     lib = load_library()
-    if q is None and k is None:
-        raise ValueError("q and k are both None")
     ref = k if q is None else q
     if not isinstance(ref, torch.Tensor) or not ref.is_cuda:
-        raise ValueError("q and k must be CUDA tensors")
-    dt, dev = ref.dtype, ref.device
-    if dt not in _DTYPE:
+        raise ValueError("q and k must be CUDA tensors (one of them may be None)")
+    dt, dev = ref.dtype, ref.get_device()
+    code = _DTYPE.get(dt)
+    if code is None:
         raise ValueError("unsupported dtype %s" % dt)
-    views, outs, shape = [], [], None
-    for x, out, nm in ((q, q_out, "q"), (k, k_out, "k")):
-        if x is None:
-            views.append((ViewStruct(), ViewStruct()))
-            outs.append(None)
-            continue
-        B, T, H, Dh, sb, st, sh = _head_rows(x, nm, dt, dev)
-        if shape is None:
-            shape = (x.dim(), B, T, Dh)
-        elif shape != (x.dim(), B, T, Dh):
+    qv = kv = qo = ko = _NO_VIEW
+    if q is not None:
+        shape, qv = _head_view(q, "q", dt, dev)
+        if q_out is None:
+            q_out, qo = _new_head_view(shape, dt, ref.device)
+        else:
+            qo = _head_view(q_out, "q_out", dt, dev, shape)[1]
+    else:
+        q_out = q_weight = None
+    if k is not None:
+        ks, kv = _head_view(k, "k", dt, dev)
+        if q is not None and (len(ks) != len(shape) or ks[:-2] != shape[:-2] or ks[-1] != shape[-1]):
             raise ValueError("q and k must agree in batch, tokens and head size")
-        if out is None:
-            out = torch.empty(x.shape, dtype=dt, device=dev)
-        elif out.shape != x.shape:
-            raise ValueError("%s_out must have the shape of %s" % (nm, nm))
-        _, _, _, _, ob, ot, oh = _head_rows(out, nm + "_out", dt, dev)
-        views.append((ViewStruct(x.data_ptr(), sb, st, sh, H), ViewStruct(out.data_ptr(), ob, ot, oh, H)))
-        outs.append(out)
-    _, B, T, Dh = shape
-    for w, nm in ((q_weight, "q_weight"), (k_weight, "k_weight")):
+        shape = ks
+        if k_out is None:
+            k_out, ko = _new_head_view(ks, dt, ref.device)
+        else:
+            ko = _head_view(k_out, "k_out", dt, dev, ks)[1]
+    else:
+        k_out = k_weight = None
+    B, T, Dh = shape[0], shape[1] if len(shape) == 4 else 1, shape[-1]
+    for w, nm, n in ((q_weight, "q_weight", Dh), (k_weight, "k_weight", Dh), (inv_freq, "inv_freq", None)):
         if w is not None:
             _need(w, nm, torch.float32)
-            if w.shape != (Dh,) or w.device != dev:
-                raise ValueError("%s must be [Dh] on %s" % (nm, dev))
-    rot = 0
-    if inv_freq is not None:
-        _need(inv_freq, "inv_freq", torch.float32)
-        if inv_freq.dim() != 1 or inv_freq.device != dev:
-            raise ValueError("inv_freq must be [rot / 2] on %s" % dev)
-        rot = 2 * inv_freq.numel()
+            if w.dim() != 1 or (n is not None and w.numel() != n) or w.get_device() != dev:
+                raise ValueError("%s must be [%s] on cuda:%d" % (nm, "rot / 2" if n is None else "Dh", dev))
     per_token = 0
     if positions is not None:
         _need(positions, "positions", torch.int32)
-        if positions.device != dev or tuple(positions.shape) not in ((B,), (B, T)):
-            raise ValueError("positions must be int32 [B] or [B, T] on %s" % dev)
-        per_token = 1 if positions.dim() == 2 else 0
+        ps = tuple(positions.shape)
+        if (ps != (B,) and ps != (B, T)) or positions.get_device() != dev:
+            raise ValueError("positions must be int32 [B] or [B, T] on cuda:%d" % dev)
+        per_token = len(ps) - 1
     with _on(dev):
         _check("ratp_qk_norm_rope", lib.ratp_qk_norm_rope(
-            views[0][0], views[1][0], views[0][1], views[1][1], _ptr(q_weight if q is not None else None),
-            _ptr(k_weight if k is not None else None), _ptr(inv_freq), _ptr(positions), per_token, B, T, Dh, rot,
-            1 if interleaved else 0, float(eps), _DTYPE[dt], _stream(ref)))
-    return tuple(outs)
+            qv, kv, qo, ko, _addr(q_weight), _addr(k_weight), _addr(inv_freq), _addr(positions), per_token, B, T, Dh,
+            0 if inv_freq is None else 2 * inv_freq.numel(), 1 if interleaved else 0, eps, code, _stream(ref)))
+    return q_out, k_out
 
 
 def _linear_args(q, k, v, log_decay, states, out, dims):
@@ -531,19 +535,20 @@ def _linear_args(q, k, v, log_decay, states, out, dims):
         raise ValueError("q must be a CUDA tensor of %d dimensions" % dims)
     if out is None:
         out = torch.empty_like(q)
+    sh, dev = q.shape, q.get_device()
     for t, nm in ((q, "q"), (k, "k"), (v, "v"), (out, "out")):
         _need(t, nm, torch.bfloat16)
-        if t.shape != q.shape or t.device != q.device:
+        if t.shape != sh or t.get_device() != dev:
             raise ValueError("q, k, v and out must have one shape, on one device")
-    B, H, Dh = q.shape[0], q.shape[-2], q.shape[-1]
+    B, H, Dh = sh[0], sh[-2], sh[-1]
     _need(log_decay, "log_decay", torch.float32)
-    if log_decay.shape != (H,) or log_decay.device != q.device:
-        raise ValueError("log_decay must be [H] on %s" % q.device)
+    if log_decay.shape != (H,) or log_decay.get_device() != dev:
+        raise ValueError("log_decay must be [H] on cuda:%d" % dev)
     for s, nm in states:
         if s is not None:
             _need(s, nm, torch.float32)
-            if s.shape != (B, H, Dh, Dh) or s.device != q.device:
-                raise ValueError("%s must be [B, H, Dh, Dh] on %s" % (nm, q.device))
+            if s.shape != (B, H, Dh, Dh) or s.get_device() != dev:
+                raise ValueError("%s must be [B, H, Dh, Dh] on cuda:%d" % (nm, dev))
     return out
 
 
@@ -561,7 +566,7 @@ def linear_attn_prefill(q, k, v, log_decay, initial_state=None, final_state=None
     lib = load_library()
     out = _linear_args(q, k, v, log_decay, ((initial_state, "initial_state"), (final_state, "final_state")), out, 4)
     B, T, H, Dh = q.shape
-    with _on(q.device):
+    with _on(q.get_device()):
         if workspace is None:
             n = linear_attn_workspace_bytes(B, T, H, Dh)
             workspace = torch.empty(n, dtype=torch.uint8, device=q.device) if n else None
@@ -588,7 +593,7 @@ def linear_attn_step(q, k, v, log_decay, state, scale=None, out=None):
         raise ValueError("state must be a CUDA tensor")
     out = _linear_args(q, k, v, log_decay, ((state, "state"),), out, 3)
     B, H, Dh = q.shape
-    with _on(q.device):
+    with _on(q.get_device()):
         _check("ratp_linear_attn_step", lib.ratp_linear_attn_step(
             q.data_ptr(), k.data_ptr(), v.data_ptr(), log_decay.data_ptr(), state.data_ptr(), out.data_ptr(), B, H, Dh,
             Dh ** -0.5 if scale is None else scale, RATP_BF16, _stream(q)))
@@ -640,9 +645,14 @@ class KVCache:
         _check(size, getattr(lib, size)(B, H, Dh, T_max, D, W, mp, ctypes.byref(n)))
         self.buffer = torch.empty(n.value, dtype=torch.uint8, device=device)
         self.c = CacheStruct()
-        _check(init, getattr(lib, init)(
-            ctypes.byref(self.c), _ptr(self.buffer), n.value, B, H, Dh, T_max, D, W, mp,
-            _stream(self.buffer)))
+        with _on(self.buffer.get_device()):
+            _check(init, getattr(lib, init)(
+                ctypes.byref(self.c), _ptr(self.buffer), n.value, B, H, Dh, T_max, D, W, mp,
+                _stream(self.buffer)))
+        self._mask_ptr = mp
+        self._ref = ctypes.byref(self.c)
+        self._len = self._view(self.c.len, B, torch.int32)
+        self._rings = {}
         self.L = int(L)
         _check("ratp_cache_set_chunk_local", lib.ratp_cache_set_chunk_local(ctypes.byref(self.c), self.L))
 
@@ -656,10 +666,10 @@ class KVCache:
         4-bit cache the fp32 values that the held rows stand for."""
         if self.kv_bits == 4:
             out = torch.empty(self.B, self.c.rows_per_b, self.Dh, dtype=torch.float32, device=self.buffer.device)
-            with _on(out.device):
+            with _on(out.get_device()):
                 _check("ratp_cache_read_q4", load_library().ratp_cache_read_q4(
-                    ctypes.byref(self.c), _ptr(out) if which == "k" else None,
-                    None if which == "k" else _ptr(out), _stream(out)))
+                    self._ref, out.data_ptr() if which == "k" else None,
+                    None if which == "k" else out.data_ptr(), _stream(out)))
             return out
         addr = self.c.Kc if which == "k" else self.c.Vc
         rows = self.B * self.c.rows_per_b
@@ -669,12 +679,16 @@ class KVCache:
         """Kw or Vw as [B, H, W, Dh] bf16 (None when W == 0)."""
         if self.W == 0:
             return None
-        addr = self.c.Kw if which == "k" else self.c.Vw
-        n = self.B * self.H * self.W * self.Dh
-        return self._view(addr, n, torch.bfloat16).view(self.B, self.H, self.W, self.Dh)
+        ring = self._rings.get(which)
+        if ring is None:
+            addr = self.c.Kw if which == "k" else self.c.Vw
+            n = self.B * self.H * self.W * self.Dh
+            ring = self._view(addr, n, torch.bfloat16).view(self.B, self.H, self.W, self.Dh)
+            self._rings[which] = ring
+        return ring
 
     def lengths(self):
-        return self._view(self.c.len, self.B, torch.int32)
+        return self._len
 
     def head_rows(self, h):
         """(offset, capacity) of head h inside one batch item's dilated rows."""
@@ -690,8 +704,9 @@ class KVCache:
         _need(hk, "hk", torch.bfloat16)
         _need(hv, "hv", torch.bfloat16)
         T = hk.shape[1] if T is None else T
-        _check("ratp_cache_pack", load_library().ratp_cache_pack(
-            ctypes.byref(self.c), _ptr(hk), _ptr(hv), int(T), _stream(hk)))
+        with _on(hk.get_device()):
+            _check("ratp_cache_pack", load_library().ratp_cache_pack(
+                self._ref, _ptr(hk), _ptr(hv), int(T), _stream(hk)))
 
     def attach_window(self, L):
         """Continue a fixed look-back recurrence of window L at decode: keeps a
@@ -720,10 +735,10 @@ class KVCache:
         if out is None:
             out = torch.empty_like(q)
         _need(out, "out", torch.bfloat16)
-        _check("ratp_decode_step", load_library().ratp_decode_step(
-            _ptr(q), _ptr(xk), _ptr(xv), _ptr(g), _ptr(state), ctypes.byref(self.c), _ptr(out),
-            self.D, self.W, ctypes.cast(self._mask_buf, ctypes.c_void_p) if self._mask_buf is not None else None,
-            _stream(q)))
+        with _on(q.get_device()):
+            _check("ratp_decode_step", load_library().ratp_decode_step(
+                q.data_ptr(), xk.data_ptr(), xv.data_ptr(), g.data_ptr(), state.data_ptr(), self._ref, out.data_ptr(),
+                self.D, self.W, self._mask_ptr, _stream(q)))
         return out
 
 
