@@ -54,7 +54,7 @@ constexpr int kThreads = 448;
 constexpr int kStateWarps = 8;         // warps 4 .. 11
 constexpr int kProducerWarp = 12;
 constexpr int kMmaWarp = 13;
-constexpr int kSlots = 5;
+constexpr int kSlots = 6;
 constexpr int kPart = 32;               // tokens whose scaled K is handed to the MMA at a time
 constexpr int kParts = C / kPart;
 constexpr int kRecurrentTokens = 16;
@@ -69,15 +69,11 @@ template <int DH>
 struct Layout {
   static constexpr uint32_t kHalf = C * 128;             // 128 rows x 64 bf16
   static constexpr uint32_t kTile = (DH / 64) * kHalf;
-  static constexpr uint32_t kPartHalf = kPart * 128;     // 32 rows x 64 bf16
-  static constexpr uint32_t kPartTile = (DH / 64) * kPartHalf;
-  // second and third term of the scaled K: two buffers of two tiles of 32 rows
-  static constexpr uint32_t kOffLo = kSlots * kTile;
-  static constexpr uint32_t kOffS = kOffLo + 4 * kPartTile;  // S, bf16 [DH / 64][DH rows][64]
+  static constexpr uint32_t kOffS = kSlots * kTile;      // S, bf16 [DH / 64][DH rows][64]
   static constexpr uint32_t kSHalf = DH * 128;
   static constexpr uint32_t kOffPow = kOffS + (DH / 64) * kSHalf;    // a^0 .. a^128
   static constexpr uint32_t kOffBar = kOffPow + (C + 1) * 4 + 4;
-  static constexpr int kBars = 2 * kSlots + 14;
+  static constexpr int kBars = 2 * kSlots + 15;
   static constexpr uint32_t kOffCtl = kOffBar + kBars * 8;           // TMEM address, abort flag
   // one CTA per SM whatever DH, since each takes all of TMEM
   static constexpr uint32_t kBytes = (kOffCtl + 8 + 1024) > 120 * 1024 ? (kOffCtl + 8 + 1024) : 120 * 1024;
@@ -86,6 +82,11 @@ static_assert(Layout<128>::kBytes <= 232448, "shared memory of one CTA");
 
 constexpr uint32_t kTmemCols = 512;
 constexpr uint32_t kColP = 0;          // 128 columns: Q K^T, then P as bf16 pairs in the first 64
+constexpr uint32_t kColO = 128;        // DH columns: Q S, scaled, += P V
+constexpr uint32_t kColS = 256;        // DH columns: the state's products (with <DH, false> at 0 and 128)
+constexpr uint32_t kColK = 384;        // 2 buffers x 3 terms x 16 columns: scaled K^T of 32 tokens
+constexpr uint32_t kTermCols = kPart / 2;
+constexpr uint32_t kBufCols = 3 * kTermCols;
 
 struct Params {
   __nv_bfloat16* o;
@@ -119,7 +120,6 @@ chunk_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ C
   constexpr int NH = DH / 64;                            // 64-channel halves
   constexpr int kUnits = OUT ? 3 : 2;                    // tiles per chunk: (Q,) K, V
   constexpr int kK = OUT ? 1 : 0;                        // K's place among them
-  constexpr uint32_t kColO1 = 128, kColO2 = kColO1 + DH, kColS = kColO2 + DH;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   const uint32_t sb = smem_u32(smem);
@@ -134,10 +134,11 @@ chunk_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ C
   // chunk c's state products done, and (<DH, false>) their TMEM buffer read:
   // barriers [c & 1], phase c / 2
   const uint32_t b_pd = b_qk + 80, b_sf = b_qk + 96;
+  const uint32_t b_qs = b_qk + 112;                      // Q S done
   float* s_pow = reinterpret_cast<float*>(smem + L::kOffPow);
   uint32_t* s_tmem = reinterpret_cast<uint32_t*>(smem + L::kOffCtl);
   volatile int* s_abort = reinterpret_cast<volatile int*>(smem + L::kOffCtl + 4);
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;   // warp: known uniform
 
   // segment `seg` of (b, h)
   const int per = OUT ? p.n_seg : p.n_seg - 1;
@@ -159,6 +160,7 @@ chunk_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ C
       mbar_init(b_empty + 8 * i, 1);
     }
     mbar_init(b_qk, 1);
+    mbar_init(b_qs, 1);
     mbar_init(b_p, 128);
     mbar_init(b_o, 1);
     mbar_init(b_ofree, 128);
@@ -188,39 +190,49 @@ chunk_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ C
   auto tile = [&](int u) { return sb + (uint32_t)(u % kSlots) * L::kTile; };
 
   auto kv_wait = [&](int g) { return mbar_wait(b_kv + 8 * (g & 1), (uint32_t)(g >> 1) & 1u, s_abort); };
-  // a^{n-1-j} k_j for parts first, first + step, .. of chunk c by one group of
-  // 128 threads: the first term in place, the others into the part's buffer
-  // (free once the products of the part that used it are done); zero rows past
-  // the sequence stay zero.  A part is a chain of latencies (the buffer, the
-  // loads, the stores' fence), so two groups work on two parts at a time.
-  auto scale_k = [&](int c, int tid, int first, int step) -> bool {
-    const int m = tokens(c);
-    uint8_t* t = smem + (uint32_t)((c * kUnits + kK) % kSlots) * L::kTile;
+  // a^{n-1-j} k_j, transposed, into TMEM (lane = channel, two tokens a column)
+  // as three bf16 terms, for parts first, first + step, .. of chunk c by a
+  // group of four warps: each takes the 32 channels of its TMEM lanes, 16 at a
+  // time, straight from K's tile by transposing loads.  A part's buffer is free
+  // once the products of the part before the last are done.
+  auto scale_k = [&](int c, int first, int step) -> bool {
+    const int m = tokens(c), quad = warp & 3, pair = lane & 3;
+    const uint32_t t = tile(c * kUnits + kK) + (uint32_t)(quad >> 1) * L::kHalf;
+    // this lane's row of the four 8 x 8 tiles (token, 16-byte chunk) of a load
+    const int row = (lane >> 4) * 8 + (lane & 7), ch = (quad & 1) * 4 + ((lane >> 3) & 1);
 #pragma unroll 1
     for (int part = first; part < kParts; part += step) {
       const int g = c * kParts + part;
       if (g >= 2 && !warp_all(kv_wait(g - 2))) return false;
-      uint8_t* lo = smem + L::kOffLo + (uint32_t)(g & 1) * 2 * L::kPartTile;
+      tc_fence_after();
+      if (32 * quad < DH) {
+        float2 w[kPart / 8];                   // weights of tokens 8 i + 2 pair, + 1
 #pragma unroll
-      for (int it = 0; it < NH * kPart * 8 / 128; ++it) {
-        const int i = tid + it * 128;
-        const int hf = i / (kPart * 8), in = i % (kPart * 8);   // 16 bytes of row in / 8 (swizzled within it)
-        uint4* src = reinterpret_cast<uint4*>(t + hf * L::kHalf + part * L::kPartHalf + in * 16);
-        uint4* dst = reinterpret_cast<uint4*>(lo + hf * L::kPartHalf + in * 16);
-        const float w = s_pow[max(m - 1 - part * kPart - in / 8, 0)];
-        const float2 w2 = make_float2(w, w);
-        float2 f[4];
-        Elem<__nv_bfloat16>::unpack2(*src, f);
-        uint4 v0, v1, v2;
-        split3(f[0], w2, &v0.x, &v1.x, &v2.x);
-        split3(f[1], w2, &v0.y, &v1.y, &v2.y);
-        split3(f[2], w2, &v0.z, &v1.z, &v2.z);
-        split3(f[3], w2, &v0.w, &v1.w, &v2.w);
-        *src = v0;
-        *dst = v1;
-        *reinterpret_cast<uint4*>(reinterpret_cast<uint8_t*>(dst) + L::kPartTile) = v2;
+        for (int i = 0; i < kPart / 8; ++i) {
+          const int e = m - 1 - (part * kPart + 8 * i + 2 * pair);
+          w[i] = make_float2(s_pow[max(e, 0)], s_pow[max(e - 1, 0)]);   // tokens past the sequence are zero
+        }
+        const uint32_t dst = tmem + ((uint32_t)(quad * 32) << 16) + kColK + (uint32_t)(g & 1) * kBufCols;
+#pragma unroll
+        for (int lh = 0; lh < 2; ++lh) {       // channels 16 lh .. of this warp's 32
+          uint32_t raw[8], t0[8], t1[8], t2[8];
+#pragma unroll
+          for (int x = 0; x < 2; ++x) {        // tokens 16 x ..
+            const int tok = part * kPart + 16 * x + row;
+            ldmatrix_x4_trans(t + (uint32_t)tok * 128 + (uint32_t)(((ch + 2 * lh) ^ (tok & 7)) * 16), raw + 4 * x);
+          }
+#pragma unroll
+          for (int x = 0; x < 8; ++x)          // register x: tokens 8 (x / 2) + 2 pair, + 1
+            split3(make_float2(__uint_as_float(raw[x] << 16), __uint_as_float(raw[x] & 0xffff0000u)), w[x / 2], &t0[x],
+                   &t1[x], &t2[x]);
+          const uint32_t d = dst + ((uint32_t)(16 * lh) << 16);
+          tmem_st_16x128b_x4(d, t0);
+          tmem_st_16x128b_x4(d + kTermCols, t1);
+          tmem_st_16x128b_x4(d + 2 * kTermCols, t2);
+        }
+        tmem_wait_st();
       }
-      asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+      tc_fence_before();
       mbar_arrive(b_kp + 8 * (g & 1));
     }
     return true;
@@ -255,83 +267,95 @@ chunk_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ C
     __syncwarp();
   } else if (warp == kMmaWarp) {
     // ------------------------------------------------------------ MMA issuer
-    if (lane == 0) {
-      constexpr uint32_t idP = idesc_bf16_f32(C, C, 0, 0);       // Q K^T: both K-major
-      constexpr uint32_t idO1 = idesc_bf16_f32(C, DH, 0, 1);     // Q S: S is [dk][dv], N-major
-      constexpr uint32_t idO2 = idesc_bf16_f32(C, DH, 0, 1);     // P V: P in TMEM
-      constexpr uint32_t idS = idesc_bf16_f32(128, DH, 1, 1);    // K'^T V: K' is [token][dk], M-major
-      bool ok = true;
-      auto issue_qk = [&](int c) -> bool {
-        const int uq = c * kUnits, uk = uq + 1;
-        if (!full_wait(uq) || !full_wait(uk)) return false;
-        tc_fence_after();
-        const uint64_t dq = sw128_desc(tile(uq), 16, 1024), dk = sw128_desc(tile(uk), 16, 1024);
+    // (the whole warp waits, one elected lane issues)
+    constexpr uint32_t idP = idesc_bf16_f32(C, C, 0, 0);         // Q K^T: both K-major
+    constexpr uint32_t idO = idesc_bf16_f32(C, DH, 0, 1);        // Q S and P V: S and V are N-major
+    // K'^T V: K' in TMEM; M is 128 for DH = 64 too, lanes 64..127 of both are not used
+    constexpr uint32_t idS = idesc_bf16_f32(128, DH, 0, 1);
+    bool ok = true;
+    auto issue_qk = [&](int c) -> bool {
+      const int uq = c * kUnits, uk = uq + 1;
+      if (!warp_all(full_wait(uq) && full_wait(uk))) return false;
+      tc_fence_after();
+      const uint64_t dq = sw128_desc(tile(uq), 16, 1024), dk = sw128_desc(tile(uk), 16, 1024);
+      if (elect_one()) {
 #pragma unroll
         for (int k = 0; k < DH / 16; ++k) {
           const uint64_t off = (uint64_t)(((k >> 2) * L::kHalf + (k & 3) * 32) >> 4);
           umma_f16(tmem + kColP, dq + off, dk + off, idP, k > 0 ? 1u : 0u);
         }
         umma_commit(b_qk);
-        return true;
-      };
-      if (OUT && !issue_qk(0)) ok = false;
-      for (int c = 0; c < n && ok; ++c) {
-        const int uk = c * kUnits + kK, uv = uk + 1;
-        const uint32_t par = (uint32_t)c & 1u;
-        const uint64_t dv = sw128_desc(tile(uv), L::kHalf, 1024);
-        if (OUT) {
-          const int uq = uk - 1;
-          if (!mbar_wait(b_s, par, s_abort) || (c > 0 && !mbar_wait(b_ofree, par ^ 1u, s_abort))) { ok = false; break; }
-          tc_fence_after();
-          const uint64_t dq = sw128_desc(tile(uq), 16, 1024), ds = sw128_desc(sb + L::kOffS, L::kSHalf, 1024);
+      }
+      __syncwarp();
+      return true;
+    };
+    if (OUT) ok = issue_qk(0);
+    for (int c = 0; c < n && ok; ++c) {
+      const int uk = c * kUnits + kK, uv = uk + 1;
+      const uint32_t par = (uint32_t)c & 1u;
+      const uint64_t dv = sw128_desc(tile(uv), L::kHalf, 1024);
+      if (OUT) {
+        const int uq = uk - 1;
+        if (!warp_all(mbar_wait(b_s, par, s_abort) && (c == 0 || mbar_wait(b_ofree, par ^ 1u, s_abort)))) { ok = false; break; }
+        tc_fence_after();
+        const uint64_t dq = sw128_desc(tile(uq), 16, 1024), ds = sw128_desc(sb + L::kOffS, L::kSHalf, 1024);
+        if (elect_one()) {
 #pragma unroll
           for (int k = 0; k < DH / 16; ++k) {
             const uint64_t off = (uint64_t)(((k >> 2) * L::kHalf + (k & 3) * 32) >> 4);
-            umma_f16(tmem + kColO1, dq + off, ds + (uint64_t)((k * 16 * 128) >> 4), idO1, k > 0 ? 1u : 0u);
+            umma_f16(tmem + kColO, dq + off, ds + (uint64_t)((k * 16 * 128) >> 4), idO, k > 0 ? 1u : 0u);
           }
+          umma_commit(b_qs);
           umma_commit(b_empty + 8 * (uq % kSlots));
-          if (!mbar_wait(b_p, par, s_abort) || !full_wait(uv)) { ok = false; break; }
-          tc_fence_after();
-#pragma unroll
-          for (int k = 0; k < C / 16; ++k)
-            umma_f16_ts(tmem + kColO2, tmem + kColP + k * 8, dv + (uint64_t)((k * 16 * 128) >> 4), idO2, k > 0 ? 1u : 0u);
-          umma_commit(b_o);
         }
-        const uint32_t tS = tmem + (OUT ? kColS : (uint32_t)(c & 1) * 128u);
-        if (!OUT && (!full_wait(uv) || (c >= 2 && !mbar_wait(b_sf + 8 * (c & 1), (uint32_t)((c >> 1) - 1) & 1u, s_abort)))) {
-          ok = false;
-          break;
-        }
+        __syncwarp();
+      }
+      if (!warp_all(full_wait(uv) &&
+                    (OUT || c < 2 || mbar_wait(b_sf + 8 * (c & 1), (uint32_t)((c >> 1) - 1) & 1u, s_abort)))) {
+        ok = false;
+        break;
+      }
+      const uint32_t tS = tmem + (OUT ? kColS : (uint32_t)(c & 1) * 128u);
 #pragma unroll 1
-        for (int part = 0; part < kParts; ++part) {
-          if (OUT && part == 1 && c + 1 < n && !issue_qk(c + 1)) { ok = false; break; }
-          if (c >= n_state) continue;
-          const int g = c * kParts + part;
-          if (!mbar_wait(b_kp + 8 * (g & 1), (uint32_t)(g >> 1) & 1u, s_abort)) { ok = false; break; }
-          tc_fence_after();
-          const uint32_t lo = sb + L::kOffLo + (uint32_t)(g & 1) * 2 * L::kPartTile;
-          const uint64_t db = dv + (uint64_t)(part * L::kPartHalf >> 4);
+      for (int part = 0; part < kParts && c < n_state; ++part) {
+        const int g = c * kParts + part;
+        if (!warp_all(mbar_wait(b_kp + 8 * (g & 1), (uint32_t)(g >> 1) & 1u, s_abort))) { ok = false; break; }
+        tc_fence_after();
+        const uint32_t ta = tmem + kColK + (uint32_t)(g & 1) * kBufCols;
+        const uint64_t db = dv + (uint64_t)(part * kPart * 128 >> 4);
+        if (elect_one()) {
 #pragma unroll
-          for (int term = 0; term < 3; ++term) {
-            // K' is [token][dk]; M is 128 for DH = 64 too: both halves of M read
-            // the same 64 channels, and lanes 64..127 of the result are not used
-            const uint64_t da = term == 0 ? sw128_desc(tile(uk) + part * L::kPartHalf, DH == 128 ? L::kHalf : 0, 1024)
-                                          : sw128_desc(lo + (term - 1) * L::kPartTile, DH == 128 ? L::kPartHalf : 0, 1024);
+          for (int term = 0; term < 3; ++term)
 #pragma unroll
             for (int k = 0; k < kPart / 16; ++k)
-              umma_f16(tS, da + (uint64_t)((k * 16 * 128) >> 4), db + (uint64_t)((k * 16 * 128) >> 4), idS,
-                       part + term + k > 0 ? 1u : 0u);
-          }
+              umma_f16_ts(tS, ta + term * kTermCols + k * 8, db + (uint64_t)((k * 16 * 128) >> 4), idS,
+                          part + term + k > 0 ? 1u : 0u);
           umma_commit(b_kv + 8 * (g & 1));
         }
-        if (!ok) break;
+        __syncwarp();
+      }
+      if (!ok) break;
+      // P is there and O holds the scaled Q S.  These products and the next
+      // chunk's Q K^T run while the state warps bring S forward.
+      if (OUT && !warp_all(mbar_wait(b_p, par, s_abort))) { ok = false; break; }
+      tc_fence_after();
+      if (elect_one()) {
         if (c < n_state) umma_commit(b_pd + 8 * (c & 1));
+        if (OUT) {
+#pragma unroll
+          for (int k = 0; k < C / 16; ++k)
+            umma_f16_ts(tmem + kColO, tmem + kColP + k * 8, dv + (uint64_t)((k * 16 * 128) >> 4), idO, 1u);
+          umma_commit(b_o);
+        }
         umma_commit(b_empty + 8 * (uk % kSlots));
         umma_commit(b_empty + 8 * (uv % kSlots));
       }
-      umma_commit(b_final);                              // all MMAs done before TMEM is released
-      mbar_drain(b_final, 0);
+      __syncwarp();
+      if (OUT && c + 1 < n && !issue_qk(c + 1)) { ok = false; break; }
     }
+    if (elect_one()) umma_commit(b_final);               // all MMAs done before TMEM is released
+    __syncwarp();
+    mbar_drain(b_final, 0);
     __syncwarp();
   } else if (warp < 4) {
     const uint32_t tl = tmem + ((uint32_t)(warp * 32) << 16);
@@ -383,6 +407,23 @@ chunk_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ C
           }
           tmem_st16(tl + kColP + 16 * q, w);             // over columns this warp has read
         }
+        // O = scale a^{i+1} Q S, onto which the tensor cores add P V
+        if (!warp_all(mbar_wait(b_qs, (uint32_t)c & 1u, s_abort))) return false;
+        tc_fence_after();
+        const float2 a2 = make_float2(ai, ai);
+#pragma unroll 2
+        for (int q = 0; q < DH / 32; ++q) {
+          uint32_t r[32];
+          tmem_ld32(tl + kColO + 32 * q, r);
+          tmem_wait_ld();
+#pragma unroll
+          for (int x = 0; x < 32; x += 2) {
+            const float2 y = mul2(a2, make_float2(__uint_as_float(r[x]), __uint_as_float(r[x + 1])));
+            r[x] = __float_as_uint(y.x);
+            r[x + 1] = __float_as_uint(y.y);
+          }
+          tmem_st32(tl + kColO + 32 * q, r);
+        }
         tmem_wait_st();
         tc_fence_before();
         mbar_arrive(b_p);
@@ -394,20 +435,13 @@ chunk_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ C
         const int t = (c0 + c) * C + i;
         __nv_bfloat16* orow = p.o + (((size_t)b * p.T + t) * p.H + h) * DH;
         const bool there = t < p.T && RATP_IN((((long long)b * p.T + t) * p.H + h) * DH, DH, (long long)p.B * p.T * p.H * DH);
-        const float2 a2 = make_float2(ai, ai);
 #pragma unroll 1
         for (int q = 0; q < DH / 32; ++q) {
-          uint32_t r1[32], r2[32];
-          tmem_ld32(tl + kColO1 + 32 * q, r1);
-          tmem_ld32(tl + kColO2 + 32 * q, r2);
+          uint32_t r[32], y[16];
+          tmem_ld32(tl + kColO + 32 * q, r);
           tmem_wait_ld();
-          uint32_t y[16];
 #pragma unroll
-          for (int x = 0; x < 16; ++x) {
-            const float2 v = fma2(a2, make_float2(__uint_as_float(r1[2 * x]), __uint_as_float(r1[2 * x + 1])),
-                                  make_float2(__uint_as_float(r2[2 * x]), __uint_as_float(r2[2 * x + 1])));
-            y[x] = pack_bf16x2(v.x, v.y);
-          }
+          for (int x = 0; x < 16; ++x) y[x] = pack_bf16x2(__uint_as_float(r[2 * x]), __uint_as_float(r[2 * x + 1]));
           if (there) {
             __nv_bfloat16* dst = orow + 32 * q;
             if (p.o_align32) {
@@ -427,13 +461,12 @@ chunk_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ C
         mbar_arrive(b_ofree);
         return true;
       };
-      // P of the next chunk before this one's output: its products come first
-      bool ok = work_p(0);
-      for (int c = 0; c < n && ok; ++c) ok = (c + 1 >= n || work_p(c + 1)) && work_o(c);
+      for (int c = 0; c < n; ++c)
+        if (!work_p(c) || !work_o(c)) break;
     } else {
       // parts 0 and 2; the state warps' second half has 1 and 3
       for (int c = 0; c < n; ++c)
-        if (!warp_all(full_wait(c * kUnits + kK)) || !scale_k(c, threadIdx.x, 0, 2)) break;
+        if (!warp_all(full_wait(c * kUnits + kK)) || !scale_k(c, 0, 2)) break;
     }
   } else {
     // ------------------------------------------------------------ state
@@ -489,9 +522,7 @@ chunk_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ C
     if (OUT) {
       publish();
       for (int c = 0; c < n_state; ++c) {
-        // K's tile is there, and Q K^T has read it
-        if (!warp_all(full_wait(c * kUnits + kK) && mbar_wait(b_qk, (uint32_t)c & 1u, s_abort)) || !scale_k(c, tid & 127, tid / 128, 2) ||
-            !products(c)) {
+        if (!warp_all(full_wait(c * kUnits + kK)) || !scale_k(c, tid / 128, 2) || !products(c)) {
           ok = false;
           break;
         }
@@ -501,7 +532,7 @@ chunk_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ C
     } else {
       // the second half's scaling runs one chunk ahead of its update
       for (int c = 0; c <= n; ++c) {
-        if ((tid >= 128 && c < n && (!warp_all(full_wait(c * kUnits + kK)) || !scale_k(c, tid & 127, 1, 2))) ||
+        if ((tid >= 128 && c < n && (!warp_all(full_wait(c * kUnits + kK)) || !scale_k(c, 1, 2))) ||
             (c > 0 && !products(c - 1))) {
           ok = false;
           break;
