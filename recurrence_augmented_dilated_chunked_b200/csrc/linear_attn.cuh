@@ -54,7 +54,7 @@ constexpr int kThreads = 448;
 constexpr int kStateWarps = 8;         // warps 4 .. 11
 constexpr int kProducerWarp = 12;
 constexpr int kMmaWarp = 13;
-constexpr int kSlots = 6;
+constexpr int kSlots = 5;
 constexpr int kPart = 32;               // tokens whose scaled K is handed to the MMA at a time
 constexpr int kParts = C / kPart;
 constexpr int kRecurrentTokens = 16;
@@ -69,7 +69,8 @@ template <int DH>
 struct Layout {
   static constexpr uint32_t kHalf = C * 128;             // 128 rows x 64 bf16
   static constexpr uint32_t kTile = (DH / 64) * kHalf;
-  static constexpr uint32_t kOffS = kSlots * kTile;      // S, bf16 [DH / 64][DH rows][64]
+  static constexpr uint32_t kOffO = kSlots * kTile;      // o of a chunk on its way out
+  static constexpr uint32_t kOffS = kOffO + kTile;       // S, bf16 [DH / 64][DH rows][64]
   static constexpr uint32_t kSHalf = DH * 128;
   static constexpr uint32_t kOffPow = kOffS + (DH / 64) * kSHalf;    // a^0 .. a^128
   static constexpr uint32_t kOffBar = kOffPow + (C + 1) * 4 + 4;
@@ -89,7 +90,6 @@ constexpr uint32_t kTermCols = kPart / 2;
 constexpr uint32_t kBufCols = 3 * kTermCols;
 
 struct Params {
-  __nv_bfloat16* o;
   const float* log_decay;              // [H]
   const float* init;                   // [B][H][DH][DH] or NULL: the state before the sequence
   float* fin;                          // [B][H][DH][DH] or NULL: the state after it
@@ -97,7 +97,6 @@ struct Params {
   int B, T, H;
   int n_chunks, seg_chunks, n_seg;
   float scale;
-  int o_align32;
 };
 
 // x * w of two floats as three bf16 terms each: every term is what the ones
@@ -111,10 +110,21 @@ __device__ __forceinline__ void split3(float2 x, float2 w, uint32_t* t0, uint32_
   *t2 = pack_bf16x2(r.x, r.y);
 }
 
+// Named barrier `id` of `count` threads; true where every one of them passed true.
+__device__ __forceinline__ bool group_all(int id, int count, bool ok) {
+  uint32_t r;
+  asm volatile(
+      "{\n\t.reg .pred p, q;\n\tsetp.ne.u32 p, %1, 0;\n\t"
+      "barrier.cta.red.and.pred q, %2, %3, p;\n\tselp.u32 %0, 1, 0, q;\n\t}"
+      : "=r"(r) : "r"((uint32_t)ok), "r"(id), "r"(count) : "memory");
+  return r != 0;
+}
+
 template <int DH, bool OUT>
 __global__ void __launch_bounds__(kThreads, 1)
 chunk_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
-             const __grid_constant__ CUtensorMap tm_v, const __grid_constant__ Params p) {
+             const __grid_constant__ CUtensorMap tm_v, const __grid_constant__ CUtensorMap tm_o,
+             const __grid_constant__ Params p) {
   using namespace sm100;
   using L = Layout<DH>;
   constexpr int NH = DH / 64;                            // 64-channel halves
@@ -184,7 +194,6 @@ chunk_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ C
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = *s_tmem;
-
   // tile u of this CTA (chunk u / kUnits; (Q,) K, V in turn) lies in slot u % kSlots
   auto full_wait = [&](int u) { return mbar_wait(b_full + 8 * (u % kSlots), (uint32_t)(u / kSlots) & 1u, s_abort); };
   auto tile = [&](int u) { return sb + (uint32_t)(u % kSlots) * L::kTile; };
@@ -206,29 +215,29 @@ chunk_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ C
       if (g >= 2 && !warp_all(kv_wait(g - 2))) return false;
       tc_fence_after();
       if (32 * quad < DH) {
-        float2 w[kPart / 8];                   // weights of tokens 8 i + 2 pair, + 1
-#pragma unroll
-        for (int i = 0; i < kPart / 8; ++i) {
-          const int e = m - 1 - (part * kPart + 8 * i + 2 * pair);
-          w[i] = make_float2(s_pow[max(e, 0)], s_pow[max(e - 1, 0)]);   // tokens past the sequence are zero
-        }
         const uint32_t dst = tmem + ((uint32_t)(quad * 32) << 16) + kColK + (uint32_t)(g & 1) * kBufCols;
 #pragma unroll
-        for (int lh = 0; lh < 2; ++lh) {       // channels 16 lh .. of this warp's 32
-          uint32_t raw[8], t0[8], t1[8], t2[8];
+        for (int x = 0; x < 2; ++x) {          // tokens 16 x .. of the part
+          const int tok = part * kPart + 16 * x + row;
+          float2 w[2];                         // weights of tokens 8 i + 2 pair, + 1
 #pragma unroll
-          for (int x = 0; x < 2; ++x) {        // tokens 16 x ..
-            const int tok = part * kPart + 16 * x + row;
-            ldmatrix_x4_trans(t + (uint32_t)tok * 128 + (uint32_t)(((ch + 2 * lh) ^ (tok & 7)) * 16), raw + 4 * x);
+          for (int i = 0; i < 2; ++i) {
+            const int e = m - 1 - (part * kPart + 16 * x + 8 * i + 2 * pair);
+            w[i] = make_float2(s_pow[max(e, 0)], s_pow[max(e - 1, 0)]);     // tokens past the sequence are zero
           }
 #pragma unroll
-          for (int x = 0; x < 8; ++x)          // register x: tokens 8 (x / 2) + 2 pair, + 1
-            split3(make_float2(__uint_as_float(raw[x] << 16), __uint_as_float(raw[x] & 0xffff0000u)), w[x / 2], &t0[x],
-                   &t1[x], &t2[x]);
-          const uint32_t d = dst + ((uint32_t)(16 * lh) << 16);
-          tmem_st_16x128b_x4(d, t0);
-          tmem_st_16x128b_x4(d + kTermCols, t1);
-          tmem_st_16x128b_x4(d + 2 * kTermCols, t2);
+          for (int lh = 0; lh < 2; ++lh) {     // channels 16 lh .. of this warp's 32
+            uint32_t raw[4], t0[4], t1[4], t2[4];
+            ldmatrix_x4_trans(t + (uint32_t)tok * 128 + (uint32_t)(((ch + 2 * lh) ^ (tok & 7)) * 16), raw);
+#pragma unroll
+            for (int y = 0; y < 4; ++y)        // register y: tokens 8 (y / 2) + 2 pair, + 1
+              split3(make_float2(__uint_as_float(raw[y] << 16), __uint_as_float(raw[y] & 0xffff0000u)), w[y / 2], &t0[y],
+                     &t1[y], &t2[y]);
+            const uint32_t d = dst + ((uint32_t)(16 * lh) << 16) + 8 * x;
+            tmem_st_16x128b_x2(d, t0);
+            tmem_st_16x128b_x2(d + kTermCols, t1);
+            tmem_st_16x128b_x2(d + 2 * kTermCols, t2);
+          }
         }
         tmem_wait_st();
       }
@@ -368,7 +377,12 @@ chunk_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ C
       // a^{i - 32q - 31} a^{31 - jj}; on it, 2^(log2(a) (i - j)) at P's bf16
       // precision.
       const float ai = s_pow[i + 1] * p.scale;
-      const float l2a = fmaxf(ld, -1.0e4f) * 1.4426950408889634f;
+      // (a decay below 2^-160 a token is none of it: a^1 is zero in fp32 either
+      // way, and the bound keeps the exponents' rounding below P's)
+      const float l2a = fmaxf(ld * 1.4426950408889634f, -160.f);
+      const float top = log2f(fabsf(p.scale));           // on the diagonal: |scale| 2^(l2a (i - j)), at most |scale|
+      const float base = fmaf(l2a, (float)lane, top);
+      const uint32_t flip = p.scale < 0.f ? 0x80008000u : 0u;
       float row[3];
 #pragma unroll
       for (int q = 0; q < 3; ++q) row[q] = s_pow[max(i - 32 * q - 31, 0)] * p.scale;
@@ -395,10 +409,9 @@ chunk_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ C
             } else {
 #pragma unroll
               for (int x = 0; x < 16; ++x) {             // branch-free: a masked value is cut off by its bits
-                const int d0 = lane - 2 * x, d1 = d0 - 1;
-                const float y0 = __uint_as_float(r[2 * x]) * (p.scale * exp2f(l2a * (float)max(d0, 0)));
-                const float y1 = __uint_as_float(r[2 * x + 1]) * (p.scale * exp2f(l2a * (float)max(d1, 0)));
-                w[x] = pack_bf16x2(y0, y1) & ~((uint32_t)(d0 >> 31) & 0xffffu) & ~((uint32_t)(d1 >> 31) & 0xffff0000u);
+                const float e0 = fminf(fmaf(-2.f * x, l2a, base), top), e1 = fminf(fmaf(-2.f * x - 1.f, l2a, base), top);
+                const float y0 = __uint_as_float(r[2 * x]) * exp2f(e0), y1 = __uint_as_float(r[2 * x + 1]) * exp2f(e1);
+                w[x] = (pack_bf16x2(y0, y1) ^ flip) & (2 * x + 1 <= lane ? 0xffffffffu : 2 * x <= lane ? 0xffffu : 0u);
               }
             }
           } else {
@@ -429,40 +442,46 @@ chunk_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ C
         mbar_arrive(b_p);
         return true;
       };
-      auto work_o = [&](int c) -> bool {
-        if (!warp_all(mbar_wait(b_o, (uint32_t)c & 1u, s_abort))) return false;
+      // o through a staging tile, so that a copy writes whole rows
+      auto work_o = [&](int c) {
         tc_fence_after();
-        const int t = (c0 + c) * C + i;
-        __nv_bfloat16* orow = p.o + (((size_t)b * p.T + t) * p.H + h) * DH;
-        const bool there = t < p.T && RATP_IN((((long long)b * p.T + t) * p.H + h) * DH, DH, (long long)p.B * p.T * p.H * DH);
-#pragma unroll 1
+#pragma unroll 2
         for (int q = 0; q < DH / 32; ++q) {
-          uint32_t r[32], y[16];
+          uint32_t r[32];
           tmem_ld32(tl + kColO + 32 * q, r);
           tmem_wait_ld();
+          if (q + 1 == DH / 32) {
+            tc_fence_before();
+            mbar_arrive(b_ofree);                        // O is read
+          }
+          uint8_t* dst = smem + L::kOffO + (q / 2) * L::kHalf + i * 128;
 #pragma unroll
-          for (int x = 0; x < 16; ++x) y[x] = pack_bf16x2(__uint_as_float(r[2 * x]), __uint_as_float(r[2 * x + 1]));
-          if (there) {
-            __nv_bfloat16* dst = orow + 32 * q;
-            if (p.o_align32) {
+          for (int v = 0; v < 4; ++v) {
+            uint32_t y[4];
 #pragma unroll
-              for (int v = 0; v < 16; v += 8)
-                asm volatile("st.global.v8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};"
-                             :: "l"(dst + 2 * v), "r"(y[v]), "r"(y[v + 1]), "r"(y[v + 2]), "r"(y[v + 3]), "r"(y[v + 4]),
-                                "r"(y[v + 5]), "r"(y[v + 6]), "r"(y[v + 7]) : "memory");
-            } else {
-#pragma unroll
-              for (int v = 0; v < 16; v += 4)
-                *reinterpret_cast<uint4*>(dst + 2 * v) = make_uint4(y[v], y[v + 1], y[v + 2], y[v + 3]);
-            }
+            for (int x = 0; x < 4; ++x)
+              y[x] = pack_bf16x2(__uint_as_float(r[8 * v + 2 * x]), __uint_as_float(r[8 * v + 2 * x + 1]));
+            *reinterpret_cast<uint4*>(dst + ((((q & 1) * 4 + v) ^ (i & 7)) * 16)) = make_uint4(y[0], y[1], y[2], y[3]);
           }
         }
-        tc_fence_before();
-        mbar_arrive(b_ofree);
-        return true;
+        asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+        group_all(1, 128, true);
+        if (threadIdx.x == 0) {                          // rows past the sequence are not written
+#pragma unroll
+          for (int hf = 0; hf < NH; ++hf)
+            tma_store_4d(&tm_o, sb + L::kOffO + hf * L::kHalf, 64 * hf, h, (c0 + c) * C, b);
+          asm volatile("cp.async.bulk.commit_group;" ::: "memory");
+        }
       };
-      for (int c = 0; c < n; ++c)
-        if (!work_p(c) || !work_o(c)) break;
+      for (int c = 0; c < n; ++c) {
+        const bool there = work_p(c) && warp_all(mbar_wait(b_o, (uint32_t)c & 1u, s_abort));
+        // the copy of the chunk before has read the staging tile; the four warps
+        // go on, or give up, together
+        if (threadIdx.x == 0) asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory");
+        if (!group_all(1, 128, there)) break;
+        work_o(c);
+      }
+      if (threadIdx.x == 0) asm volatile("cp.async.bulk.wait_group 0;" ::: "memory");
     } else {
       // parts 0 and 2; the state warps' second half has 1 and 3
       for (int c = 0; c < n; ++c)

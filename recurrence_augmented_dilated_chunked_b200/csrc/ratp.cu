@@ -615,13 +615,14 @@ bool make_chunk_map(CUtensorMap* m, const void* base, int B, int T, int H, int D
 
 template <int DH>
 int launch_linear_chunks(const LinearPlan& pl, const CUtensorMap& tq, const CUtensorMap& tk, const CUtensorMap& tv,
+                         const CUtensorMap& to,
                          const linear_attn::Params& p, cudaStream_t st) {
   using namespace linear_attn;
   constexpr int smem = (int)Layout<DH>::kBytes;
   const long long pairs = (long long)p.B * p.H;
   if (pl.n_seg > 1) {
     if (!ensure_smem(chunk_kernel<DH, false>, smem)) return RATP_ERR_CUDA;
-    chunk_kernel<DH, false><<<(unsigned)(pairs * (pl.n_seg - 1)), kThreads, smem, st>>>(tq, tk, tv, p);
+    chunk_kernel<DH, false><<<(unsigned)(pairs * (pl.n_seg - 1)), kThreads, smem, st>>>(tq, tk, tv, to, p);
     int rc = launch_status();
     if (rc) return rc;
     const int quads = DH * DH / 4;
@@ -635,7 +636,7 @@ int launch_linear_chunks(const LinearPlan& pl, const CUtensorMap& tq, const CUte
     }
   }
   if (!ensure_smem(chunk_kernel<DH, true>, smem)) return RATP_ERR_CUDA;
-  chunk_kernel<DH, true><<<(unsigned)(pairs * pl.n_seg), kThreads, smem, st>>>(tq, tk, tv, p);
+  chunk_kernel<DH, true><<<(unsigned)(pairs * pl.n_seg), kThreads, smem, st>>>(tq, tk, tv, to, p);
   return launch_status();
 }
 
@@ -1110,7 +1111,6 @@ int ratp_linear_attn_prefill(const void* q, const void* k, const void* v, const 
   }
   linear_attn::Params p;
   memset(&p, 0, sizeof(p));
-  p.o = static_cast<__nv_bfloat16*>(o);
   p.log_decay = log_decay;
   p.init = initial_state;
   p.fin = final_state;
@@ -1118,11 +1118,12 @@ int ratp_linear_attn_prefill(const void* q, const void* k, const void* v, const 
   p.B = B; p.T = T; p.H = H;
   p.n_chunks = pl.n_chunks; p.seg_chunks = pl.seg_chunks; p.n_seg = pl.n_seg;
   p.scale = scale;
-  p.o_align32 = (reinterpret_cast<uintptr_t>(o) & 31u) == 0;
-  CUtensorMap tq, tk, tv;
-  if (!make_chunk_map(&tq, q, B, T, H, Dh) || !make_chunk_map(&tk, k, B, T, H, Dh) || !make_chunk_map(&tv, v, B, T, H, Dh))
+  CUtensorMap tq, tk, tv, to;
+  if (!make_chunk_map(&tq, q, B, T, H, Dh) || !make_chunk_map(&tk, k, B, T, H, Dh) || !make_chunk_map(&tv, v, B, T, H, Dh) ||
+      !make_chunk_map(&to, o, B, T, H, Dh))
     return RATP_ERR_CUDA;
-  return Dh == 128 ? launch_linear_chunks<128>(pl, tq, tk, tv, p, st) : launch_linear_chunks<64>(pl, tq, tk, tv, p, st);
+  return Dh == 128 ? launch_linear_chunks<128>(pl, tq, tk, tv, to, p, st)
+                   : launch_linear_chunks<64>(pl, tq, tk, tv, to, p, st);
 }
 
 int ratp_linear_attn_step(const void* q, const void* k, const void* v, const float* log_decay,
