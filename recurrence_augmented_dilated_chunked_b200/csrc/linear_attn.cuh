@@ -99,15 +99,19 @@ struct Params {
   float scale;
 };
 
-// x * w of two floats as three bf16 terms each: every term is what the ones
-// before leave, which fp32 holds exactly (x has 8 bits, w 24).
+// x * w of two floats as three bf16 terms each, which are its fp32 value's upper,
+// middle and lower 8 bits (cut off, not rounded, so that every remainder is
+// exact and the third term leaves nothing).
 __device__ __forceinline__ void split3(float2 x, float2 w, uint32_t* t0, uint32_t* t1, uint32_t* t2) {
+  auto upper = [](float2 v) { return __byte_perm(__float_as_uint(v.x), __float_as_uint(v.y), 0x7632); };
+  auto cut = [](float2 v) {
+    return make_float2(__uint_as_float(__float_as_uint(v.x) & 0xffff0000u), __uint_as_float(__float_as_uint(v.y) & 0xffff0000u));
+  };
   const float2 y = mul2(x, w);
-  *t0 = pack_bf16x2(y.x, y.y);
-  float2 r = fma2(x, w, make_float2(-__uint_as_float(*t0 << 16), -__uint_as_float(*t0 & 0xffff0000u)));
-  *t1 = pack_bf16x2(r.x, r.y);
-  r = sub2(r, make_float2(__uint_as_float(*t1 << 16), __uint_as_float(*t1 & 0xffff0000u)));
-  *t2 = pack_bf16x2(r.x, r.y);
+  *t0 = upper(y);
+  const float2 r = sub2(y, cut(y));
+  *t1 = upper(r);
+  *t2 = upper(sub2(r, cut(r)));
 }
 
 // Named barrier `id` of `count` threads; true where every one of them passed true.
@@ -212,27 +216,39 @@ chunk_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ C
 #pragma unroll 1
     for (int part = first; part < kParts; part += step) {
       const int g = c * kParts + part;
-      if (g >= 2 && !warp_all(kv_wait(g - 2))) return false;
-      tc_fence_after();
-      if (32 * quad < DH) {
-        const uint32_t dst = tmem + ((uint32_t)(quad * 32) << 16) + kColK + (uint32_t)(g & 1) * kBufCols;
+      // everything is loaded before the buffer is waited for
+      const bool mine = 32 * quad < DH;
+      uint32_t raw[16];
+      float2 w[4];                             // weights of tokens 8 i + 2 pair, + 1
+      if (mine) {
 #pragma unroll
         for (int x = 0; x < 2; ++x) {          // tokens 16 x .. of the part
           const int tok = part * kPart + 16 * x + row;
-          float2 w[2];                         // weights of tokens 8 i + 2 pair, + 1
 #pragma unroll
-          for (int i = 0; i < 2; ++i) {
-            const int e = m - 1 - (part * kPart + 16 * x + 8 * i + 2 * pair);
-            w[i] = make_float2(s_pow[max(e, 0)], s_pow[max(e - 1, 0)]);     // tokens past the sequence are zero
-          }
+          for (int lh = 0; lh < 2; ++lh)       // channels 16 lh .. of this warp's 32
+            ldmatrix_x4_trans(t + (uint32_t)tok * 128 + (uint32_t)(((ch + 2 * lh) ^ (tok & 7)) * 16), raw + 8 * x + 4 * lh);
+        }
 #pragma unroll
-          for (int lh = 0; lh < 2; ++lh) {     // channels 16 lh .. of this warp's 32
-            uint32_t raw[4], t0[4], t1[4], t2[4];
-            ldmatrix_x4_trans(t + (uint32_t)tok * 128 + (uint32_t)(((ch + 2 * lh) ^ (tok & 7)) * 16), raw);
+        for (int i = 0; i < 4; ++i) {
+          const int e = m - 1 - (part * kPart + 8 * i + 2 * pair);
+          w[i] = make_float2(s_pow[max(e, 0)], s_pow[max(e - 1, 0)]);       // tokens past the sequence are zero
+        }
+      }
+      if (g >= 2 && !warp_all(kv_wait(g - 2))) return false;
+      tc_fence_after();
+      if (mine) {
+        const uint32_t dst = tmem + ((uint32_t)(quad * 32) << 16) + kColK + (uint32_t)(g & 1) * kBufCols;
 #pragma unroll
-            for (int y = 0; y < 4; ++y)        // register y: tokens 8 (y / 2) + 2 pair, + 1
-              split3(make_float2(__uint_as_float(raw[y] << 16), __uint_as_float(raw[y] & 0xffff0000u)), w[y / 2], &t0[y],
+        for (int x = 0; x < 2; ++x) {
+#pragma unroll
+          for (int lh = 0; lh < 2; ++lh) {
+            uint32_t t0[4], t1[4], t2[4];
+#pragma unroll
+            for (int y = 0; y < 4; ++y) {      // register y: tokens 8 (y / 2) + 2 pair, + 1
+              const uint32_t v = raw[8 * x + 4 * lh + y];
+              split3(make_float2(__uint_as_float(v << 16), __uint_as_float(v & 0xffff0000u)), w[2 * x + y / 2], &t0[y],
                      &t1[y], &t2[y]);
+            }
             const uint32_t d = dst + ((uint32_t)(16 * lh) << 16) + 8 * x;
             tmem_st_16x128b_x2(d, t0);
             tmem_st_16x128b_x2(d + kTermCols, t1);

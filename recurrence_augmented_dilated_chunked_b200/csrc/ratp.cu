@@ -537,11 +537,11 @@ struct LinearPlan {
   int n_chunks, seg_chunks, n_seg;
 };
 
-// Chunks per segment.  One pass over a segment's chunks with output costs
-// about 2 us per chunk, the pass for its state alone 1 us, a CTA's start and
-// end 3 us and the extra launches 4 us; the plan is the cheapest number of
-// segments under that model (128 (b, h) of 64 chunks: one segment each; 32 of
-// 128 chunks: four).
+// Chunks per segment.  Measured: the pass with output takes 3.7 us a chunk, the
+// pass for the state alone 2 us, a CTA's start and end 4 us, the two extra
+// launches 6 us; the plan is the cheapest number of segments under that model
+// (128 (b, h) of 64 chunks: one segment each; 32 of 128 chunks: four, 186 us
+// against 480 us in one).
 int linear_plan(int B, int T, int H, int Dh, LinearPlan* pl) {
   if (B < 0 || T < 0 || H < 0) return RATP_ERR_ARG;
   if (Dh != 64 && Dh != 128) return RATP_ERR_SHAPE;
@@ -556,8 +556,8 @@ int linear_plan(int B, int T, int H, int Dh, LinearPlan* pl) {
   for (int want = 1; want <= std::min(pl->n_chunks, 256); ++want) {
     const int sc = (pl->n_chunks + want - 1) / want, ns = (pl->n_chunks + sc - 1) / sc;
     if (ns != want) continue;
-    long long cost = (pairs * ns + slots - 1) / slots * (2 * sc + 3);
-    if (ns > 1) cost += (pairs * (ns - 1) + slots - 1) / slots * (sc + 3) + 4;
+    long long cost = (pairs * ns + slots - 1) / slots * (37 * sc + 40);
+    if (ns > 1) cost += (pairs * (ns - 1) + slots - 1) / slots * (20 * sc + 40) + 60;
     if (want == 1 || cost < best) {
       best = cost;
       pl->seg_chunks = sc;
