@@ -85,13 +85,22 @@ __device__ __forceinline__ int head_of_split(const Params& p, int rem) {
   return lo;
 }
 
-// The recurrence step of (b, h) for both streams, by the CTA's kThreads
-// threads: new fp32 state, the bf16-rounded key/value into s_self_k /
+// The recurrence step of (b, h) for both streams, by the CTA's NT threads: new fp32 state, the bf16-rounded key/value into s_self_k /
 // s_self_v and the ring, and append(stream, channel, value) for each channel
 // (the caller's cached row).  Ends with a barrier.
-template <int DH, typename Append>
+struct StepInput {
+  float x, g, prev;             // input, gate and fp32 state of one channel
+};
+__device__ __forceinline__ StepInput load_input(const Params& p, long long bh, int s, int ch, int dh) {
+  return {__bfloat162float((s == 0 ? p.xk : p.xv)[bh * dh + ch]), __bfloat162float(p.g[bh * dh + ch]),
+          p.state[((long long)s * p.B * p.H + bh) * dh + ch]};
+}
+
+// early: this thread's inputs if they are loaded already (channel tid + NT i
+// in early[i]), else NULL.
+template <int DH, int NT, typename Append>
 __device__ __forceinline__ void recurrence_step(const Params& p, long long bh, int t, float* s_self_k, float* s_self_v,
-                                                Append append) {
+                                                const StepInput* early, Append append) {
   const int tid = threadIdx.x;
   [[maybe_unused]] const long long n_tok = (long long)p.B * p.H * DH;
   [[maybe_unused]] const long long n_ring = (long long)p.B * p.H * p.W * DH;
@@ -100,7 +109,7 @@ __device__ __forceinline__ void recurrence_step(const Params& p, long long bh, i
   if (WL > 0) {
     // this step's inputs into slot t mod WL; the window is then
     // positions max(0, t - WL + 1) .. t of the ring
-    for (int c = tid; c < 3 * DH; c += kThreads) {
+    for (int c = tid; c < 3 * DH; c += NT) {
       const int s3 = c / DH, ch = c % DH;
       const __nv_bfloat16* src = (s3 == 0 ? p.xk : s3 == 1 ? p.xv : p.g) + bh * DH + ch;
       const long long dst = (((long long)s3 * p.B * p.H + bh) * WL + t % WL) * DH + ch;
@@ -108,13 +117,14 @@ __device__ __forceinline__ void recurrence_step(const Params& p, long long bh, i
     }
     __syncthreads();
   }
-  for (int c = tid; c < 2 * DH; c += kThreads) {
+#pragma unroll
+  for (int i = 0; i < 2 * DH / NT; ++i) {
+    const int c = tid + i * NT;
     const int s = c / DH, ch = c % DH;
     if (!RATP_IN(((long long)s * p.B * p.H + bh) * DH + ch, 1, 2 * n_tok) ||
         !RATP_IN(bh * DH + ch, 1, n_tok)) continue;
+    const StepInput in = early != nullptr ? early[i] : load_input(p, bh, s, ch, DH);
     float* st = p.state + ((long long)s * p.B * p.H + bh) * DH + ch;
-    const float x = __bfloat162float((s == 0 ? p.xk : p.xv)[bh * DH + ch]);
-    const float gg = __bfloat162float(p.g[bh * DH + ch]);
     float hn;
     if (WL > 0) {
       // fixed look-back: the recurrence from zero over the window
@@ -132,8 +142,8 @@ __device__ __forceinline__ void recurrence_step(const Params& p, long long bh, i
       }
       hn = acc_h;
     } else {
-      const float prev = (p.reset_L > 0 && t % p.reset_L == 0) ? 0.f : *st;
-      hn = fmaf(gg, prev - x, x);
+      const float prev = (p.reset_L > 0 && t % p.reset_L == 0) ? 0.f : in.prev;
+      hn = fmaf(in.g, prev - in.x, in.x);
     }
     *st = hn;
     const __nv_bfloat16 hb = __float2bfloat16_rn(hn);
@@ -148,7 +158,7 @@ __device__ __forceinline__ void recurrence_step(const Params& p, long long bh, i
 // Merges the CTA's NG entries (running max s_m, sum s_l, accumulator s_acc; a
 // barrier precedes the call) and writes o, or this split's partial; the last
 // split of (b, h) to publish merges the partials.
-template <int DH, int NG>
+template <int DH, int NG, int NT>
 __device__ __forceinline__ void merge_entries(const Params& p, long long bh, int split, int n_used, const float* s_m,
                                               const float* s_l, const float (*s_acc)[DH], int* s_last) {
   const int tid = threadIdx.x;
@@ -160,7 +170,7 @@ __device__ __forceinline__ void merge_entries(const Params& p, long long bh, int
   [[maybe_unused]] const long long n_part = (long long)p.B * p.H * p.max_splits * (DH + 2);
   const bool part_ok = single || RATP_IN((bh * p.max_splits + split) * (DH + 2), DH + 2, n_part);
   float* part = p.partial + (bh * p.max_splits + split) * (DH + 2);
-  for (int c = tid; c < DH; c += kThreads) {
+  for (int c = tid; c < DH; c += NT) {
     float L = 0.f, A = 0.f;
 #pragma unroll
     for (int gi = 0; gi < NG; ++gi) {
@@ -189,7 +199,7 @@ __device__ __forceinline__ void merge_entries(const Params& p, long long bh, int
       const bool pb_ok = RATP_IN(bh * p.max_splits * (DH + 2), (long long)n_used * (DH + 2), n_part);
       float MM = -INFINITY;
       for (int i = 0; i < n_used; ++i) MM = fmaxf(MM, __ldcg(pb + i * (DH + 2)));
-      for (int c = tid; pb_ok && c < DH; c += kThreads) {
+      for (int c = tid; pb_ok && c < DH; c += NT) {
         float L = 0.f, A = 0.f;
         for (int i = 0; i < n_used; ++i) {
           const float mi = __ldcg(pb + i * (DH + 2));
@@ -206,18 +216,17 @@ __device__ __forceinline__ void merge_entries(const Params& p, long long bh, int
 
 // The last CTA of batch item b advances len[b] (one counter per batch item,
 // so the step's closing atomics spread over B addresses instead of one).
+// Each CTA has read len[b], and used what it read, before its arrival, so the
+// counter alone orders the update after the reads.
 __device__ __forceinline__ void advance_len(const Params& p, int b) {
   __syncthreads();
   if (threadIdx.x == 0) {
-    __threadfence();
     uint32_t* cnt = p.counters + (long long)p.B * p.H + b;
     const unsigned int prev = atomicAdd(cnt, 1u);
     if (prev == (unsigned int)p.splits_per_b - 1u) {
-      __threadfence();
       const int tb = p.len[b];
       if (tb < p.T_max) p.len[b] = tb + 1;
       *cnt = 0u;
-      __threadfence();
     }
   }
 }
@@ -296,7 +305,7 @@ decode_kernel(const Params p) {
       const bool keep = t % Dd == Dd - 1;
       if (keep && app_slot >= p.T_max / Dd && tid == 0) raise_error(RATP_ERR_CAPACITY);
       const bool room = keep && app_slot < p.T_max / Dd;
-      recurrence_step<DH>(p, bh, t, s_self_k, s_self_v, [&](int s, int ch, __nv_bfloat16 hb) {
+      recurrence_step<DH, kThreads>(p, bh, t, s_self_k, s_self_v, nullptr, [&](int s, int ch, __nv_bfloat16 hb) {
         if (room && RATP_IN((cache_row0 + app_slot) * DH + ch, 1, n_dil))
           (s == 0 ? p.Kc : p.Vc)[(cache_row0 + app_slot) * DH + ch] = hb;
       });
@@ -401,7 +410,7 @@ decode_kernel(const Params p) {
 #pragma unroll
     for (int i = 0; i < 8; ++i) s_acc[grp][li * 8 + i] = acc[i];
     __syncthreads();
-    merge_entries<DH, NG>(p, bh, split, n_used, s_m, s_l, s_acc, &s_last);
+    merge_entries<DH, NG, kThreads>(p, bh, split, n_used, s_m, s_l, s_acc, &s_last);
   }
 
   advance_len(p, b);

@@ -42,13 +42,15 @@
 namespace ratp {
 namespace decode_q4 {
 
-constexpr int kThreads = 128;
+// Two warps per CTA: eight CTAs per SM hold more (b, h) at once than four of
+// twice the size, and each has its own start and end to wait through.
+constexpr int kThreads = 64;
 constexpr int kWarps = kThreads / 32;
 constexpr int kTile = 16;          // keys per MMA tile
 constexpr int kStep = 32;          // cached rows per warp step
 constexpr int kRingStep = 8;       // ring rows per warp step (their bytes fit the same stage)
 constexpr int kStages = 2;         // steps in flight per warp
-constexpr int kCtasPerSm = 4;
+constexpr int kCtasPerSm = 8;
 constexpr int kGroup = 32;         // channels per scale
 // A ring key moves 512 bytes where a 4-bit key moves 160: it counts as three
 // when a (b, h)'s keys are split over CTAs.
@@ -536,8 +538,6 @@ __device__ __forceinline__ void attend_ring(Acc<DH>& a, const RingStage<DH>& st,
 
 static_assert(sizeof(RingStage<128>) <= sizeof(Stage<128>) && sizeof(RingStage<64>) <= sizeof(Stage<64>), "stage");
 
-__device__ __forceinline__ void prefetch_l2(const void* p) { asm volatile("prefetch.global.L2 [%0];" :: "l"(p)); }
-
 template <int DH>
 __global__ void __launch_bounds__(kThreads, kCtasPerSm)
 decode_kernel(const Params pp) {
@@ -581,6 +581,22 @@ decode_kernel(const Params pp) {
   }
   asm volatile("griddepcontrol.wait;" ::: "memory");
   const int t = p.len[b];
+  // the query and the recurrence's inputs: on their way with the length, ahead
+  // of the cache stream
+  const long long bh = (long long)b * p.H + h;
+  [[maybe_unused]] const long long n_tok = (long long)p.B * p.H * DH;
+  const int warp = tid >> 5, lane = tid & 31, g = lane >> 2, tq = lane & 3;
+  const bool q_ok = RATP_IN(bh * DH, DH, n_tok);
+  uint4 qv[DH / 32];                           // this lane's quarter of the channels
+#pragma unroll
+  for (int i = 0; i < DH / 32; ++i)
+    qv[i] = q_ok ? reinterpret_cast<const uint4*>(p.q + bh * DH + tq * (DH / 4))[i] : make_uint4(0u, 0u, 0u, 0u);
+  constexpr int kIn = 2 * DH / kThreads;
+  decode::StepInput in[kIn];
+  if (split == 0 && q_ok) {
+#pragma unroll
+    for (int i = 0; i < kIn; ++i) in[i] = decode::load_input(p, bh, (tid + i * kThreads) / DH, (tid + i * kThreads) % DH, DH);
+  }
   const int Dd = dense ? 1 : p.D;
   bool active = true;
   int n_slots = 0, w_lo = 0, n_win = 0, n_used = 1, app_slot = 0;
@@ -601,25 +617,7 @@ decode_kernel(const Params pp) {
   }
 
   if (active) {
-    const long long bh = (long long)b * p.H + h;
-    [[maybe_unused]] const long long n_tok = (long long)p.B * p.H * DH;
     [[maybe_unused]] const long long n_ring = (long long)p.B * p.H * p.W * DH;
-    const int warp = tid >> 5, lane = tid & 31, g = lane >> 2, tq = lane & 3;
-
-    // ---- the query, loaded ahead of the cache stream; then the recurrence's
-    // inputs are warmed (they are used after the stream) ----
-    const bool q_ok = RATP_IN(bh * DH, DH, n_tok);
-    uint4 qv[DH / 32];                         // this lane's quarter of the channels
-#pragma unroll
-    for (int i = 0; i < DH / 32; ++i)
-      qv[i] = q_ok ? reinterpret_cast<const uint4*>(p.q + bh * DH + tq * (DH / 4))[i] : make_uint4(0u, 0u, 0u, 0u);
-    if (split == 0 && q_ok && tid < 2 * DH / 32) {
-      // state rows (fp32, 128 bytes per thread), then x_k, x_v, g
-      const int st = tid / (DH / 32), c = tid % (DH / 32) * 32;
-      prefetch_l2(p.state + ((long long)st * p.B * p.H + bh) * DH + c);
-      prefetch_l2((st == 0 ? p.xk : p.xv) + bh * DH + c);
-      if (st == 0) prefetch_l2(p.g + bh * DH + c);
-    }
     // ---- this split's share: units [u0, u1) of slots, then of ring keys ----
     const long long u0 = (long long)split * p.split_keys, u1 = u0 + p.split_keys;
     const int s_end = (int)min((long long)n_slots, u1);
@@ -655,6 +653,26 @@ decode_kernel(const Params pp) {
     };
 #pragma unroll
     for (int i = 0; i < kStages - 1; ++i) fetch_next();
+
+    // ---- the recurrence, the appended row (the first cached rows are on their way) ----
+    if (split == 0) {
+      decode::recurrence_step<DH, kThreads>(p, bh, t, s_self[0], s_self[1], q_ok ? in : nullptr, [](int, int, __nv_bfloat16) {});
+      if (t % Dd == Dd - 1) {
+        if (app_slot >= cap) {
+          if (tid == 0) raise_error(RATP_ERR_CAPACITY);
+        } else if (tid < 2 * W8 && RATP_IN(row0 + app_slot, 1, n_rows)) {
+          // 8 channels per thread; W8 threads per stream, in whole groups of 4
+          const int st = tid / W8, w = tid % W8;
+          uint32_t par;
+          float2 f[4];
+#pragma unroll
+          for (int i = 0; i < 4; ++i) f[i] = *reinterpret_cast<const float2*>(&s_self[st][8 * w + 2 * i]);
+          const uint32_t code = quantise8(Elem<__nv_bfloat16>::pack2(f), &par, 0xfu << (lane & ~3));
+          (st == 0 ? kc : vc)[(row0 + app_slot) * W8 + w] = code;
+          if ((w & 3) == 0) (st == 0 ? pp.Kp : pp.Vp)[(row0 + app_slot) * PG + w / 4] = par;
+        }
+      }
+    }
 
     uint32_t qf[NQ][2];
     float qsum[2];
@@ -705,26 +723,6 @@ decode_kernel(const Params pp) {
       use = use + 1 == kStages ? 0 : use + 1;
     }
 
-    // ---- the recurrence, the appended row ----
-    if (split == 0) {
-      decode::recurrence_step<DH>(p, bh, t, s_self[0], s_self[1], [](int, int, __nv_bfloat16) {});
-      if (t % Dd == Dd - 1) {
-        if (app_slot >= cap) {
-          if (tid == 0) raise_error(RATP_ERR_CAPACITY);
-        } else if (tid < 2 * W8 && RATP_IN(row0 + app_slot, 1, n_rows)) {
-          // 8 channels per thread; W8 threads per stream, in whole groups of 4
-          const int st = tid / W8, w = tid % W8;
-          uint32_t par;
-          float2 f[4];
-#pragma unroll
-          for (int i = 0; i < 4; ++i) f[i] = *reinterpret_cast<const float2*>(&s_self[st][8 * w + 2 * i]);
-          const uint32_t code = quantise8(Elem<__nv_bfloat16>::pack2(f), &par, 0xfu << (lane & ~3));
-          (st == 0 ? kc : vc)[(row0 + app_slot) * W8 + w] = code;
-          if ((w & 3) == 0) (st == 0 ? pp.Kp : pp.Vp)[(row0 + app_slot) * PG + w / 4] = par;
-        }
-      }
-    }
-
     // ---- this warp's entry ----
 #pragma unroll
     for (int off = 4; off < 32; off <<= 1) a.l += __shfl_xor_sync(0xffffffffu, a.l, off);
@@ -767,7 +765,7 @@ decode_kernel(const Params pp) {
       for (int c = lane; c < DH; c += 32) s_acc[kWarps][c] = split == 0 ? s_self[1][c] : 0.f;
     }
     __syncthreads();
-    decode::merge_entries<DH, NE>(p, bh, split, n_used, s_m, s_l, s_acc, &s_last);
+    decode::merge_entries<DH, NE, kThreads>(p, bh, split, n_used, s_m, s_l, s_acc, &s_last);
   }
 
   decode::advance_len(p, b);

@@ -22,7 +22,7 @@ namespace ratp {
 namespace norm_rope {
 
 constexpr int kThreads = 128;
-constexpr int kUnroll = 4;      // heads in flight per group
+constexpr int kUnroll = 2;      // heads in flight per group
 
 struct Tensor {
   const void* x;
@@ -65,7 +65,7 @@ template <> struct Quad<float> {
 };
 
 template <typename E, int DH>
-__global__ void __launch_bounds__(kThreads)
+__global__ void __launch_bounds__(kThreads, 8)
 norm_rope_kernel(const Params p) {
   using Q = Quad<E>;
   using V = typename Q::V;

@@ -1399,6 +1399,7 @@ int decode_launch(const void* q, const void* xk, const void* xv, const void* g,
     const int smem = decode_q4::kWarps * decode_q4::kStages *
                      (int)(c->Dh == 128 ? sizeof(decode_q4::Stage<128>) : sizeof(decode_q4::Stage<64>));
     cfg.dynamicSmemBytes = smem;
+    cfg.blockDim = dim3(decode_q4::kThreads);
     auto kernel = c->Dh == 128 ? decode_q4::decode_kernel<128> : decode_q4::decode_kernel<64>;
     if (!ensure_smem(kernel, smem)) return RATP_ERR_CUDA;
     e = cudaLaunchKernelEx(&cfg, kernel, p4);
