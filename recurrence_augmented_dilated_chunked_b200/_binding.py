@@ -454,9 +454,9 @@ def _head_view(t, name, dtype, device, shape=None):
                           st[-2] if H > 1 else 0, H, 0)
 
 
-def _new_head_view(sz, dtype, device):
-    """A new dense tensor of shape ``sz`` and its packed ratp_view."""
-    t = torch.empty(sz, dtype=dtype, device=device)
+def _new_head_view(like, sz):
+    """A new dense tensor like ``like`` (of shape ``sz``) and its packed ratp_view."""
+    t = torch.empty_like(like, memory_format=torch.contiguous_format)
     H, Dh = sz[-2], sz[-1]
     T = sz[1] if len(sz) == 4 else 1
     return t, _VIEW.pack(t.data_ptr(), T * H * Dh, H * Dh, Dh, H, 0)
@@ -494,7 +494,7 @@ def qk_norm_rope(q, k, q_weight, k_weight, inv_freq, positions=None, eps=1e-6, i
     if q is not None:
         shape, qv = _head_view(q, "q", dt, dev)
         if q_out is None:
-            q_out, qo = _new_head_view(shape, dt, ref.device)
+            q_out, qo = _new_head_view(q, shape)
         else:
             qo = _head_view(q_out, "q_out", dt, dev, shape)[1]
     else:
@@ -505,7 +505,7 @@ def qk_norm_rope(q, k, q_weight, k_weight, inv_freq, positions=None, eps=1e-6, i
             raise ValueError("q and k must agree in batch, tokens and head size")
         shape = ks
         if k_out is None:
-            k_out, ko = _new_head_view(ks, dt, ref.device)
+            k_out, ko = _new_head_view(k, ks)
         else:
             ko = _head_view(k_out, "k_out", dt, dev, ks)[1]
     else:
