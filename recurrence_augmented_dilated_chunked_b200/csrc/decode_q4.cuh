@@ -487,21 +487,23 @@ __device__ __forceinline__ int ring_place(int c, int r) {
   return (c / Q + 4 * (c % Q)) ^ (((r & 1) << 2) | ((r >> 1) & 3));
 }
 
-// Ring positions pos0 .. pos0 + n - 1 (n <= kRingStep, n <= W) into a stage;
-// the rest zero.
+// n <= kRingStep ring rows from ring row `first` on (wrapping at W) into a
+// stage; the rest zero.  Chunk i of a lane is row (32 i + lane) / (DH / 8).
 template <int DH>
-__device__ __forceinline__ void fetch_ring(uint32_t stage, const __nv_bfloat16* kw, const __nv_bfloat16* vw, int pos0,
+__device__ __forceinline__ void fetch_ring(uint32_t stage, const __nv_bfloat16* kw, const __nv_bfloat16* vw, int first,
                                            int W, int n, int lane) {
-  constexpr int NC = DH / 8;
-  const int first = pos0 % W;
+  constexpr int NC = DH / 8, kRowsPer = 32 / NC;
+  const int r0 = lane / NC, c = lane % NC;
 #pragma unroll
-  for (int i = 0; i < kRingStep * NC / 32; ++i) {
-    const int r = (i * 32 + lane) / NC, c = (i * 32 + lane) % NC;
-    const int row = r < n ? (first + r < W ? first + r : first + r - W) : 0;
-    const long long src = (long long)row * DH + c * 8;
+  for (int i = 0; i < kRingStep / kRowsPer; ++i) {
+    const int r = i * kRowsPer + r0;
+    int row = first + r;
+    row = row < W ? row : row - W;
+    if (r >= n) row = first;                   // any row of the ring: not read
+    const long long off = (long long)row * (DH * 2) + c * 16;
     const uint32_t dst = stage + (uint32_t)(r * NC + ring_place<DH>(c, r)) * 16;
-    cp_async<16>(dst, kw + src, r < n);
-    cp_async<16>(dst + (uint32_t)offsetof(RingStage<DH>, v), vw + src, r < n);
+    cp_async<16>(dst, reinterpret_cast<const char*>(kw) + off, r < n);
+    cp_async<16>(dst + (uint32_t)offsetof(RingStage<DH>, v), reinterpret_cast<const char*>(vw) + off, r < n);
   }
 }
 
@@ -636,7 +638,9 @@ decode_kernel(const Params pp) {
     Walk<DH> walk;
     walk.start(kc, pp.Kp, vc, pp.Vp, row0 + k0, lane);
     int at = k0, fill = 0;                     // next cached rows to fetch, and the stage for them
-    int ring = r_begin + warp * kRingStep;     // next ring rows, after the cached ones
+    int ring = r_begin + warp * kRingStep;     // next ring rows, after the cached ones, and where they lie
+    int ring_row = n_win > 0 ? (w_lo + ring) % p.W : 0;
+    const int ring_hop = n_win > 0 ? kWarps * kRingStep % p.W : 0;
     auto fetch_next = [&]() {
       const uint32_t stage = stage0 + fill * (uint32_t)sizeof(Stage<DH>);
       if (at < s_end) {
@@ -645,8 +649,10 @@ decode_kernel(const Params pp) {
         walk.advance(kRows);
         at += kRows;
       } else if (ring < r_end) {
-        fetch_ring<DH>(stage, kw, vw, w_lo + ring, p.W, min(kRingStep, r_end - ring), lane);
+        fetch_ring<DH>(stage, kw, vw, ring_row, p.W, min(kRingStep, r_end - ring), lane);
         ring += kWarps * kRingStep;
+        ring_row += ring_hop;
+        ring_row = ring_row < p.W ? ring_row : ring_row - p.W;
       }
       asm volatile("cp.async.commit_group;" ::: "memory");
       fill = fill + 1 == kStages ? 0 : fill + 1;
@@ -750,15 +756,10 @@ decode_kernel(const Params pp) {
       float s = -INFINITY;
       if (split == 0) {
         s = 0.f;
+        if (q_ok)
+          for (int c = lane; c < DH; c += 32) s = fmaf(__bfloat162float(p.q[bh * DH + c]), s_self[0][c], s);
 #pragma unroll
-        for (int i = 0; i < DH / 32; ++i) {
-          float f[8];
-          Elem<__nv_bfloat16>::unpack(qv[i], f);
-#pragma unroll
-          for (int j = 0; j < 8; ++j) s = fmaf(f[j], s_self[0][tq * (DH / 4) + 8 * i + j], s);
-        }
-        s += __shfl_xor_sync(0xffffffffu, s, 1);       // the 4 quarters; every g computes the same
-        s += __shfl_xor_sync(0xffffffffu, s, 2);
+        for (int off = 16; off > 0; off >>= 1) s += __shfl_xor_sync(0xffffffffu, s, off);
         s *= p.scale_log2;
       }
       if (lane == 0) { s_m[kWarps] = s; s_l[kWarps] = split == 0 ? 1.f : 0.f; }

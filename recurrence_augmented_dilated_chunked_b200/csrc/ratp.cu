@@ -538,10 +538,11 @@ struct LinearPlan {
 };
 
 // Chunks per segment.  Measured: the pass with output takes 3.7 us a chunk, the
-// pass for the state alone 2 us, a CTA's start and end 4 us, the two extra
-// launches 6 us; the plan is the cheapest number of segments under that model
-// (128 (b, h) of 64 chunks: one segment each; 32 of 128 chunks: four, 186 us
-// against 480 us in one).
+// pass for the state alone 2 us, a CTA's start and end 8 us, the two extra
+// launches 6 us and 0.3 us a segment; the plan is the cheapest number of
+// segments under that model (128 (b, h) of 64 chunks: one segment each; 32 of
+// 128 chunks: four, 187 us against 202 us in nine; 15 of 8 chunks: eight, 18 us
+// against 23 us in four).
 int linear_plan(int B, int T, int H, int Dh, LinearPlan* pl) {
   if (B < 0 || T < 0 || H < 0) return RATP_ERR_ARG;
   if (Dh != 64 && Dh != 128) return RATP_ERR_SHAPE;
@@ -556,8 +557,8 @@ int linear_plan(int B, int T, int H, int Dh, LinearPlan* pl) {
   for (int want = 1; want <= std::min(pl->n_chunks, 256); ++want) {
     const int sc = (pl->n_chunks + want - 1) / want, ns = (pl->n_chunks + sc - 1) / sc;
     if (ns != want) continue;
-    long long cost = (pairs * ns + slots - 1) / slots * (37 * sc + 40);
-    if (ns > 1) cost += (pairs * (ns - 1) + slots - 1) / slots * (20 * sc + 40) + 60;
+    long long cost = (pairs * ns + slots - 1) / slots * (37 * sc + 80);
+    if (ns > 1) cost += (pairs * (ns - 1) + slots - 1) / slots * (20 * sc + 80) + 60 + 3 * ns;
     if (want == 1 || cost < best) {
       best = cost;
       pl->seg_chunks = sc;
