@@ -430,9 +430,7 @@ typedef struct ratp_cache {
                            ratp_cache_set_chunk_local */
   int32_t window_L;     /* fixed look-back window (0 = none); set by ratp_cache_set_window */
   int32_t kv_bits;      /* bits a channel of the dilated rows: 16 (bf16; 0 reads as 16) or 4
-                           (ratp_cache_init_q4: Kc, Vc hold codes, Kp, Vp their parameters) */
-  void* Kp;             /* 4-bit rows: uint32 [B * rows_per_b][Dh / 32], scale (bf16, low half) */
-  void* Vp;             /* and minimum (bf16, high half) of each 32 channels; else NULL */
+                           (ratp_cache_init_q4: Kc holds blocks of keys and values, Vc is NULL) */
   uint8_t dense[RATP_MAX_HEADS];
 } ratp_cache;
 
@@ -452,11 +450,16 @@ int ratp_cache_init(ratp_cache* c, void* buffer, size_t bytes,
  * step).  Each row is kept in groups of 32 channels; a group keeps its minimum
  * m, the step s = bf16((max - m) / 15) and the codes n = round((x - m) / s) in
  * 0..15 (round half to even; 0 where s == 0), and stands for m + n s, so that
- * a row of Dh channels takes Dh/2 + Dh/8 bytes instead of 2 Dh.  Code words:
- * uint32 [B * rows_per_b][Dh / 8] in Kc / Vc; channel c of a word's 8 sits in
- * nibble c/2 + 4 (c mod 2).  The window ring stays bf16 and the recurrent state
- * fp32, so the last W positions are read as they are.
- * Values must be finite and max - m within fp32.
+ * a row of Dh channels takes Dh/2 + Dh/8 bytes instead of 2 Dh.
+ * Layout (Kc): head h keeps its slots in ceil(cap_h / 32) blocks of 32, the
+ * heads of a batch item one after the other; a block is uint32 K codes [32]
+ * [Dh/8], V codes [32][Dh/8], K parameters [32][Dh/32], V parameters [32][Dh/32].
+ * Channel c of a code word's 8 sits in nibble c/2 + 4 (c mod 2); a parameter
+ * word is s (bf16, low half) and m (bf16, high half).  The window ring stays
+ * bf16 and the recurrent state fp32, so the last W positions are read as they
+ * are.
+ * Values must be finite, max - m within fp32, and a step s below fp32's normal
+ * range counts as 0.
  * Every other entry point takes such a cache as it takes a bf16 one
  * (ratp_cache_pack quantises; ratp_decode_step quantises the row it appends
  * and attends to the held values; ratp_decode_step_layers mixes both kinds).

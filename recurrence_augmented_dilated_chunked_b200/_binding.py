@@ -45,7 +45,6 @@ class CacheStruct(ctypes.Structure):
         ("T_max", ctypes.c_int32), ("D", ctypes.c_int32), ("W", ctypes.c_int32),
         ("split_keys", ctypes.c_int32), ("max_splits", ctypes.c_int32),
         ("reset_L", ctypes.c_int32), ("window_L", ctypes.c_int32), ("kv_bits", ctypes.c_int32),
-        ("Kp", ctypes.c_void_p), ("Vp", ctypes.c_void_p),
         ("dense", ctypes.c_uint8 * MAX_HEADS),
     ]
 

@@ -9,8 +9,12 @@
 // 128).  Codes: one 32-bit word per 8 channels; channel c of the word sits in
 // nibble c/2 + 4 (c mod 2), so that (w >> 4i) & 0x000f000f is the pair of
 // neighbouring channels 2i, 2i + 1 as two 16-bit halves.  Parameters: one
-// word per group, s in the low half, m in the high half.  The window ring
-// stays bf16 and the recurrent state fp32.
+// word per group, s in the low half, m in the high half.  The rows of 32
+// consecutive slots of a head form a block (struct Block): its K codes, V codes,
+// K parameters and V parameters one after the other, 5 KB for Dh = 128.  A block
+// is what a warp fetches at a time, so the step reads memory in long pieces (four
+// separate arrays streamed at 4.4 - 4.8 TB/s).  The window ring stays bf16 and the
+// recurrent state fp32.
 //
 // Decode step: the grid, the split of a (b, h)'s virtual key list over CTAs,
 // the recurrence in split 0 and the closing merge are those of decode.cuh.
@@ -36,6 +40,7 @@
 #pragma once
 #include "common.cuh"
 #include "decode.cuh"
+#include "sm100.cuh"
 
 #include <stddef.h>
 
@@ -55,12 +60,30 @@ constexpr int kGroup = 32;         // channels per scale
 // A ring key moves 512 bytes where a 4-bit key moves 160: it counts as three
 // when a (b, h)'s keys are split over CTAs.
 constexpr int kRingUnits = 3;
-constexpr int kPrefetchRows = 128; // rows per split warmed into L2 before the wait
+constexpr int kPrefetchBlocks = 1; // blocks per split warmed into L2 before the wait
+
+// kStep consecutive slots of one head: codes and parameters of K and V.
+template <int DH>
+struct Block {
+  uint32_t k[kStep][DH / 8];
+  uint32_t v[kStep][DH / 8];
+  uint32_t kp[kStep][DH / kGroup];
+  uint32_t vp[kStep][DH / kGroup];
+};
+
+__host__ __device__ constexpr long long blocks_of(long long cap) { return (cap + kStep - 1) / kStep; }
+
+// First block of head h inside one batch item.
+__device__ __forceinline__ long long head_block(const unsigned long long* bits, int h, int T_max, int D) {
+  int nd = 0;
+  for (int w = 0; w < (h >> 6); ++w) nd += __popcll(bits[w]);
+  if (h & 63) nd += __popcll(bits[h >> 6] & ((1ull << (h & 63)) - 1ull));
+  return nd * blocks_of(T_max) + (h - nd) * blocks_of(T_max / D);
+}
 
 struct Params {
-  decode::Params d;                // Kc / Vc hold code words, [B][rows_per_b][Dh / 8]
-  uint32_t* Kp;                    // [B][rows_per_b][Dh / 32]
-  uint32_t* Vp;
+  decode::Params d;                // Kc: Block<DH> [B][blocks_per_b]
+  long long blocks_per_b;
 };
 
 __device__ __forceinline__ float param_scale(uint32_t p) { return __uint_as_float(p << 16); }
@@ -141,8 +164,7 @@ __device__ __forceinline__ uint32_t quantise8(const uint4& x, uint32_t* par, uns
 // ---- prefill -> cache hand-off ------------------------------------------------
 struct PackParams {
   decode::PackParams d;
-  uint32_t* Kp;
-  uint32_t* Vp;
+  long long blocks_per_b;
   int base[RATP_MAX_HEADS + 1];    // first block (within a batch item) of each head
 };
 
@@ -164,7 +186,7 @@ __device__ __forceinline__ int head_at(const int* base, int H, int at) {
 constexpr int kPackRows = 4;
 template <int DH>
 __global__ void __launch_bounds__(256)
-pack_kernel(const PackParams pp) {
+pack_kernel(const __grid_constant__ PackParams pp) {
   const decode::PackParams& p = pp.d;
   constexpr int TPR = DH / 8;
   constexpr int RPB = 256 / TPR;
@@ -180,7 +202,8 @@ pack_kernel(const PackParams pp) {
   if (at == 0 && threadIdx.x == 0) p.len[b] = p.T;
   const long long src_base = (long long)b * p.T * p.H * DH + (long long)h * DH + li * 8;
   [[maybe_unused]] const long long n_src = (long long)p.B * p.T * p.H * DH;
-  const long long row0 = (long long)b * p.rows_per_b + decode::head_offset(p.dense_bits, h, p.T_max, p.D);
+  const long long block0 = (long long)b * pp.blocks_per_b + head_block(p.dense_bits, h, p.T_max, p.D);
+  Block<DH>* const blocks = reinterpret_cast<Block<DH>*>(p.Kc) + block0;
   const unsigned lanes = 0xfu << ((threadIdx.x & 31) & ~3);
 
   uint4 in[kPackRows][2];
@@ -199,14 +222,14 @@ pack_kernel(const PackParams pp) {
   for (int i = 0; i < kPackRows; ++i) {
     const int r = r0 + i * RPB;                // the same for a group's 4 lanes
     if (r < n_dil) {
-      const long long row = row0 + r;
-      if (!RATP_IN(row, 1, (long long)p.B * p.rows_per_b)) continue;
+      if (!RATP_IN(block0 + r / kStep, 1, p.B * pp.blocks_per_b)) continue;
+      Block<DH>& blk = blocks[r / kStep];
 #pragma unroll
       for (int s = 0; s < 2; ++s) {
         uint32_t par;
         const uint32_t w = quantise8(in[i][s], &par, lanes);
-        reinterpret_cast<uint32_t*>(s == 0 ? p.Kc : p.Vc)[row * (DH / 8) + li] = w;
-        if ((li & 3) == 0) (s == 0 ? pp.Kp : pp.Vp)[row * (DH / kGroup) + li / 4] = par;
+        (s == 0 ? blk.k : blk.v)[r % kStep][li] = w;
+        if ((li & 3) == 0) (s == 0 ? blk.kp : blk.vp)[r % kStep][li / 4] = par;
       }
     } else if (r < n_dil + n_ring) {
       const long long dst = (((long long)b * p.H + h) * p.W + (w_lo + (r - n_dil)) % p.W) * DH + li * 8;
@@ -218,30 +241,47 @@ pack_kernel(const PackParams pp) {
 }
 
 // ---- read-back: the values that the held rows stand for, fp32 ------------------
-// A thread takes kReadPer quads of 4 channels, a block's width apart, so that
-// every store of a warp is 512 contiguous bytes.
-constexpr int kReadPer = 4;
+// A CTA reads one block of slots; a thread has quads of 4 channels, 256 apart, so
+// that every store of a warp is 512 contiguous bytes.
+struct ReadParams {
+  const void* blocks;
+  float* out;                      // [B][rows_per_b][Dh]
+  long long rows_per_b;
+  int B, H, D, T_max, value;       // value: 0 the keys, 1 the values
+  int base[RATP_MAX_HEADS + 1];    // first block (within a batch item) of each head
+  unsigned long long dense_bits[RATP_MAX_HEADS / 64];
+};
+template <int DH>
 __global__ void __launch_bounds__(256)
-unpack_kernel(const uint32_t* __restrict__ codes, const uint32_t* __restrict__ params, float* __restrict__ out,
-              long long quads) {
-  const long long i0 = (long long)blockIdx.x * (256 * kReadPer) + threadIdx.x;
-  uint32_t w[kReadPer], par[kReadPer];
+unpack_kernel(const __grid_constant__ ReadParams p) {
+  constexpr int QPR = DH / 4, N = kStep * QPR / 256;     // quads per row, per thread
+  const int b = blockIdx.x / p.base[p.H], at = blockIdx.x - b * p.base[p.H];
+  const int h = head_at(p.base, p.H, at);
+  const int cap = decode::is_dense(p.dense_bits, h) ? p.T_max : p.T_max / p.D;
+  const int r0 = (at - p.base[h]) * kStep;
+  const Block<DH>& blk = static_cast<const Block<DH>*>(p.blocks)[blockIdx.x];
+  const uint32_t* codes = p.value ? &blk.v[0][0] : &blk.k[0][0];
+  const uint32_t* params = p.value ? &blk.vp[0][0] : &blk.kp[0][0];
+  const long long row0 = (long long)b * p.rows_per_b + decode::head_offset(p.dense_bits, h, p.T_max, p.D) + r0;
+  float4* out = reinterpret_cast<float4*>(p.out) + row0 * QPR;
+  const int n = min(kStep, cap - r0) * QPR;              // the last block of a head may be partly slots it has not
+  uint32_t w[N], par[N];
 #pragma unroll
-  for (int j = 0; j < kReadPer; ++j) {
-    const long long i = i0 + 256 * j;
-    w[j] = i < quads ? codes[i >> 1] : 0u;
-    par[j] = i < quads ? params[i >> 3] : 0u;
+  for (int j = 0; j < N; ++j) {
+    const int q = threadIdx.x + 256 * j;
+    w[j] = codes[q >> 1];
+    par[j] = params[q >> 3];
   }
 #pragma unroll
-  for (int j = 0; j < kReadPer; ++j) {
-    const long long i = i0 + 256 * j;
-    if (i >= quads) return;
+  for (int j = 0; j < N; ++j) {
+    const int q = threadIdx.x + 256 * j;
+    if (q >= n || !RATP_IN(row0 + q / QPR, 1, p.B * p.rows_per_b)) continue;
     const float s = param_scale(par[j]), m = param_min(par[j]);
-    const uint32_t x = w[j] >> ((i & 1) * 8);  // channels 4, 5, 6, 7 are the nibbles 2, 6, 3, 7
+    const uint32_t x = w[j] >> ((q & 1) * 8);  // channels 4, 5, 6, 7 are the nibbles 2, 6, 3, 7
     float f[4];
 #pragma unroll
-    for (int c = 0; c < 4; ++c) f[c] = __fadd_rn(m, __fmul_rn((float)((x >> nibble_shift(c)) & 15u), s));
-    __stcs(reinterpret_cast<float4*>(out) + i, make_float4(f[0], f[1], f[2], f[3]));
+    for (int i = 0; i < 4; ++i) f[i] = __fadd_rn(m, __fmul_rn((float)((x >> nibble_shift(i)) & 15u), s));
+    __stcs(out + q, make_float4(f[0], f[1], f[2], f[3]));
   }
 }
 
@@ -267,68 +307,20 @@ struct Lane {
   static constexpr int NV = DH / 64;           // V words per key and lane (an eighth)
 };
 
-// A warp's stage in shared memory: kStep keys' codes and parameters of K and V.
-template <int DH>
-struct Stage {
-  uint32_t k[kStep][DH / 8];
-  uint32_t v[kStep][DH / 8];
-  uint32_t kp[kStep][DH / kGroup];
-  uint32_t vp[kStep][DH / kGroup];
-};
-
-// Copies BYTES to shared memory; with there == false, zeros.
-template <int BYTES>
-__device__ __forceinline__ void cp_async(uint32_t dst, const void* src, bool there) {
-  const int n = there ? BYTES : 0;
-  if constexpr (BYTES == 16)
-    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" :: "r"(dst), "l"(src), "r"(n) : "memory");
-  else
-    asm volatile("cp.async.ca.shared.global [%0], [%1], 8, %2;" :: "r"(dst), "l"(src), "r"(n) : "memory");
+// 16 bytes to shared memory; with there == false, zeros.
+__device__ __forceinline__ void cp_async16(uint32_t dst, const void* src, bool there) {
+  const int n = there ? 16 : 0;
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" :: "r"(dst), "l"(src), "r"(n) : "memory");
 }
 
-// Copies kStep rows of W words, BYTES at a time over the warp's lanes: src and
-// dst are this lane's first chunk.  Rows from n on are not read but zeroed.
-template <int W, int BYTES>
-__device__ __forceinline__ void copy_rows(uint32_t dst, const uint32_t* src, int n, int lane) {
-  constexpr int kPer = kStep * W * 4 / (32 * BYTES);   // chunks per lane
-  static_assert(kStep * W * 4 % (32 * BYTES) == 0, "whole warps of chunks");
-  if (n == kStep) {
-#pragma unroll
-    for (int i = 0; i < kPer; ++i) cp_async<BYTES>(dst + i * 32 * BYTES, src + i * 8 * BYTES, true);
-  } else {
-#pragma unroll
-    for (int i = 0; i < kPer; ++i) {
-      const bool there = (i * 32 + lane) * BYTES / (W * 4) < n;
-      cp_async<BYTES>(dst + i * 32 * BYTES, there ? src + i * 8 * BYTES : src - lane * (BYTES / 4), there);
-    }
-  }
-}
-
-// A warp's walk over its cached rows: this lane's first chunk of each array.
+// A block into shared memory as one copy; completes on `bar`.  One thread.
 template <int DH>
-struct Walk {
-  static constexpr int W = DH / 8, P = DH / kGroup;
-  static constexpr int kParBytes = P == 4 ? 16 : 8;    // a parameter row of 8 bytes is only 8-byte aligned
-  const uint32_t *k, *kp, *v, *vp;
-  __device__ __forceinline__ void start(const uint32_t* kc, const uint32_t* kpar, const uint32_t* vc,
-                                        const uint32_t* vpar, long long row, int lane) {
-    k = kc + row * W + lane * 4;
-    v = vc + row * W + lane * 4;
-    kp = kpar + row * P + lane * (kParBytes / 4);
-    vp = vpar + row * P + lane * (kParBytes / 4);
-  }
-  __device__ __forceinline__ void fetch(uint32_t stage, int n, int lane) const {
-    using S = Stage<DH>;
-    copy_rows<W, 16>(stage + (uint32_t)offsetof(S, k) + lane * 16, k, n, lane);
-    copy_rows<P, kParBytes>(stage + (uint32_t)offsetof(S, kp) + lane * kParBytes, kp, n, lane);
-    copy_rows<W, 16>(stage + (uint32_t)offsetof(S, v) + lane * 16, v, n, lane);
-    copy_rows<P, kParBytes>(stage + (uint32_t)offsetof(S, vp) + lane * kParBytes, vp, n, lane);
-  }
-  __device__ __forceinline__ void advance(int rows) {
-    k += rows * W; v += rows * W;
-    kp += rows * P; vp += rows * P;
-  }
-};
+__device__ __forceinline__ void fetch_block(uint32_t stage, const Block<DH>* src, uint32_t bar) {
+  constexpr uint32_t kBytes = (uint32_t)sizeof(Block<DH>);
+  sm100::mbar_arrive_expect_tx(bar, kBytes);
+  asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];"
+               :: "r"(stage), "l"(src), "r"(kBytes), "r"(bar) : "memory");
+}
 
 template <int N>
 __device__ __forceinline__ void read_words(uint32_t* r, const uint32_t* src) {
@@ -407,7 +399,7 @@ __device__ __forceinline__ void gather_weights(float p0, float p1, int t, float*
 }
 
 template <int DH>
-__device__ __forceinline__ void attend_codes(Acc<DH>& a, const Stage<DH>& st, const uint32_t (*qf)[2],
+__device__ __forceinline__ void attend_codes(Acc<DH>& a, const Block<DH>& st, const uint32_t (*qf)[2],
                                              const float* qsum, float scale_log2, int n, int g, int t) {
   constexpr int NW = Lane<DH>::NW, NV = Lane<DH>::NV, P = DH / kGroup;
   constexpr int R = kStep / 8;                 // keys g + 8 r of this lane
@@ -502,8 +494,8 @@ __device__ __forceinline__ void fetch_ring(uint32_t stage, const __nv_bfloat16* 
     if (r >= n) row = first;                   // any row of the ring: not read
     const long long off = (long long)row * (DH * 2) + c * 16;
     const uint32_t dst = stage + (uint32_t)(r * NC + ring_place<DH>(c, r)) * 16;
-    cp_async<16>(dst, reinterpret_cast<const char*>(kw) + off, r < n);
-    cp_async<16>(dst + (uint32_t)offsetof(RingStage<DH>, v), reinterpret_cast<const char*>(vw) + off, r < n);
+    cp_async16(dst, reinterpret_cast<const char*>(kw) + off, r < n);
+    cp_async16(dst + (uint32_t)offsetof(RingStage<DH>, v), reinterpret_cast<const char*>(vw) + off, r < n);
   }
 }
 
@@ -538,13 +530,13 @@ __device__ __forceinline__ void attend_ring(Acc<DH>& a, const RingStage<DH>& st,
   }
 }
 
-static_assert(sizeof(RingStage<128>) <= sizeof(Stage<128>) && sizeof(RingStage<64>) <= sizeof(Stage<64>), "stage");
+static_assert(sizeof(RingStage<128>) <= sizeof(Block<128>) && sizeof(RingStage<64>) <= sizeof(Block<64>), "stage");
 
 template <int DH>
 __global__ void __launch_bounds__(kThreads, kCtasPerSm)
 decode_kernel(const Params pp) {
   const decode::Params& p = pp.d;
-  constexpr int W8 = DH / 8, PG = DH / kGroup;
+  constexpr int W8 = DH / 8;
   constexpr int NQ = DH / 16;                  // score MMAs per tile
   constexpr int NE = kWarps + 1;               // merged entries: the warps and the query's own key
 
@@ -552,7 +544,9 @@ decode_kernel(const Params pp) {
   __shared__ float s_m[NE], s_l[NE];
   __shared__ __align__(16) float s_acc[NE][DH];
   __shared__ int s_last;
-  extern __shared__ __align__(16) uint8_t s_stages[];    // Stage<DH>[kWarps][kStages]
+  __shared__ __align__(8) unsigned long long s_bar[kWarps][kStages];
+  __shared__ int s_abort;
+  extern __shared__ __align__(128) uint8_t s_stages[];   // Block<DH>[kWarps][kStages]
 
   const int b = blockIdx.x / p.splits_per_b;
   const int rem = blockIdx.x - b * p.splits_per_b;
@@ -561,26 +555,24 @@ decode_kernel(const Params pp) {
   const int tid = threadIdx.x;
   const bool dense = decode::is_dense(p.dense_bits, h);
   const int cap = dense ? p.T_max : p.T_max / p.D;
-  const long long row0 = (long long)b * p.rows_per_b + decode::head_offset(p.dense_bits, h, p.T_max, p.D);
-  [[maybe_unused]] const long long n_rows = (long long)p.B * p.rows_per_b;
-  uint32_t* const kc = reinterpret_cast<uint32_t*>(p.Kc);
-  uint32_t* const vc = reinterpret_cast<uint32_t*>(p.Vc);
+  const long long block0 = (long long)b * pp.blocks_per_b + head_block(p.dense_bits, h, p.T_max, p.D);
+  [[maybe_unused]] const long long n_blocks = (long long)p.B * pp.blocks_per_b;
+  Block<DH>* const blocks = reinterpret_cast<Block<DH>*>(p.Kc) + block0;
 
   // as in decode.cuh: let the next step be scheduled, warm L2 with this
   // split's first rows, then wait for the kernels before this one
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   if (tid == 0) {
-    const int first = min(split * p.split_keys, cap);
-    const int n = min(kPrefetchRows, cap - first);
-    if (n > 0 && RATP_IN(row0 + first, n, n_rows)) {
-      decode::bulk_prefetch_l2(kc + (row0 + first) * W8, (uint32_t)n * W8 * 4);
-      decode::bulk_prefetch_l2(vc + (row0 + first) * W8, (uint32_t)n * W8 * 4);
-      if (PG % 4 == 0) {                       // a parameter row of 16 bytes
-        decode::bulk_prefetch_l2(pp.Kp + (row0 + first) * PG, (uint32_t)n * PG * 4);
-        decode::bulk_prefetch_l2(pp.Vp + (row0 + first) * PG, (uint32_t)n * PG * 4);
-      }
-    }
+    const long long first = (long long)split * p.split_keys / kStep;
+    const long long n = min((long long)kPrefetchBlocks, blocks_of(cap) - first);
+    if (n > 0 && RATP_IN(block0 + first, n, n_blocks))
+      decode::bulk_prefetch_l2(blocks + first, (uint32_t)(n * sizeof(Block<DH>)));
+    s_abort = 0;
+#pragma unroll
+    for (int i = 0; i < kWarps * kStages; ++i) sm100::mbar_init(sm100::smem_u32(&s_bar[0][0] + i), 1);
+    sm100::fence_barrier_init();
   }
+  __syncthreads();
   asm volatile("griddepcontrol.wait;" ::: "memory");
   const int t = p.len[b];
   // the query and the recurrence's inputs: on their way with the length, ahead
@@ -626,27 +618,23 @@ decode_kernel(const Params pp) {
     const auto ring_at = [&](long long u) {
       return (int)min((long long)n_win, (max(u - n_slots, 0ll) + kRingUnits - 1) / kRingUnits);
     };
-    const int k0 = (int)min((long long)n_slots, u0) + warp * kStep;
-    Stage<DH>* const stages = reinterpret_cast<Stage<DH>*>(s_stages) + warp * kStages;
-    const uint32_t stage0 = (uint32_t)__cvta_generic_to_shared(stages);
+    const int k0 = (int)min((long long)n_slots, u0) + warp * kStep;      // u0 is whole blocks
+    Block<DH>* const stages = reinterpret_cast<Block<DH>*>(s_stages) + warp * kStages;
+    const uint32_t stage0 = sm100::smem_u32(stages), bar0 = sm100::smem_u32(&s_bar[warp][0]);
     // a warp's steps: rows k0 + i kRows .. of the cache, then its share of the
     // ring; one commit group per step, empty past the end
     constexpr int kRows = kWarps * kStep;
     const int r_begin = ring_at(u0), r_end = RATP_IN(bh * p.W * DH, (long long)p.W * DH, n_ring) ? ring_at(u1) : 0;
     const __nv_bfloat16* kw = p.Kw + bh * p.W * DH;
     const __nv_bfloat16* vw = p.Vw + bh * p.W * DH;
-    Walk<DH> walk;
-    walk.start(kc, pp.Kp, vc, pp.Vp, row0 + k0, lane);
     int at = k0, fill = 0;                     // next cached rows to fetch, and the stage for them
     int ring = r_begin + warp * kRingStep;     // next ring rows, after the cached ones, and where they lie
     int ring_row = n_win > 0 ? (w_lo + ring) % p.W : 0;
     const int ring_hop = n_win > 0 ? kWarps * kRingStep % p.W : 0;
     auto fetch_next = [&]() {
-      const uint32_t stage = stage0 + fill * (uint32_t)sizeof(Stage<DH>);
+      const uint32_t stage = stage0 + fill * (uint32_t)sizeof(Block<DH>);
       if (at < s_end) {
-        const int n = min(kStep, s_end - at);
-        if (RATP_IN(row0 + at, n, n_rows)) walk.fetch(stage, n, lane);
-        walk.advance(kRows);
+        if (lane == 0 && RATP_IN(block0 + at / kStep, 1, n_blocks)) fetch_block<DH>(stage, blocks + at / kStep, bar0 + 8 * fill);
         at += kRows;
       } else if (ring < r_end) {
         fetch_ring<DH>(stage, kw, vw, ring_row, p.W, min(kRingStep, r_end - ring), lane);
@@ -666,7 +654,7 @@ decode_kernel(const Params pp) {
       if (t % Dd == Dd - 1) {
         if (app_slot >= cap) {
           if (tid == 0) raise_error(RATP_ERR_CAPACITY);
-        } else if (tid < 2 * W8 && RATP_IN(row0 + app_slot, 1, n_rows)) {
+        } else if (tid < 2 * W8 && RATP_IN(block0 + app_slot / kStep, 1, n_blocks)) {
           // 8 channels per thread; W8 threads per stream, in whole groups of 4
           const int st = tid / W8, w = tid % W8;
           uint32_t par;
@@ -674,8 +662,9 @@ decode_kernel(const Params pp) {
 #pragma unroll
           for (int i = 0; i < 4; ++i) f[i] = *reinterpret_cast<const float2*>(&s_self[st][8 * w + 2 * i]);
           const uint32_t code = quantise8(Elem<__nv_bfloat16>::pack2(f), &par, 0xfu << (lane & ~3));
-          (st == 0 ? kc : vc)[(row0 + app_slot) * W8 + w] = code;
-          if ((w & 3) == 0) (st == 0 ? pp.Kp : pp.Vp)[(row0 + app_slot) * PG + w / 4] = par;
+          Block<DH>& blk = blocks[app_slot / kStep];
+          (st == 0 ? blk.k : blk.v)[app_slot % kStep][w] = code;
+          if ((w & 3) == 0) (st == 0 ? blk.kp : blk.vp)[app_slot % kStep][w / 4] = par;
         }
       }
     }
@@ -711,13 +700,29 @@ decode_kernel(const Params pp) {
       for (int i = 0; i < 4; ++i) a.c[j][i] = 0.f;
 
     int use = 0;
+    uint32_t phase = 0;                        // of the barrier of stage `use`
     for (int k = k0; k < s_end; k += kRows) {
       fetch_next();
-      asm volatile("cp.async.wait_group %0;" :: "n"(kStages - 1) : "memory");
-      __syncwarp();
+      if (!sm100::warp_all(sm100::mbar_wait(bar0 + 8 * use, phase, &s_abort))) {
+        // every copy under way lands before the CTA ends: this one, and the ones
+        // fetched ahead of it
+        for (int i = 0, kk = k; i < kStages && kk < s_end; ++i, kk += kRows) {
+          sm100::mbar_drain(bar0 + 8 * use, phase);
+          use = use + 1 == kStages ? 0 : use + 1;
+          phase ^= use == 0 ? 1u : 0u;
+        }
+        at = s_end;
+        break;
+      }
+      if (s_end - k < kStep) {                 // rows past the last slot hold anything: 0 times their step must be 0
+        uint32_t* par = &stages[use].vp[0][0];
+        for (int i = (s_end - k) * (DH / kGroup) + lane; i < kStep * (DH / kGroup); i += 32) par[i] = 0u;
+        __syncwarp();
+      }
       attend_codes<DH>(a, stages[use], qf, qsum, p.scale_log2, s_end - k, g, tq);
       __syncwarp();
       use = use + 1 == kStages ? 0 : use + 1;
+      phase ^= use == 0 ? 1u : 0u;
     }
     for (int r = r_begin + warp * kRingStep; r < r_end; r += kWarps * kRingStep) {
       fetch_next();

@@ -644,7 +644,7 @@ int launch_linear_chunks(const LinearPlan& pl, const CUtensorMap& tq, const CUte
 // ---- cache ------------------------------------------------------------------
 struct CacheLayout {
   long long rows_per_b;
-  size_t off_kc, off_vc, off_kw, off_vw, off_len, off_part, off_cnt, off_kp, off_vp, total;
+  size_t off_kc, off_vc, off_kw, off_vw, off_len, off_part, off_cnt, total;
   int max_splits, split_keys;
 };
 
@@ -664,11 +664,19 @@ constexpr int kMinSplitKeys = 128;
 constexpr long long kQ4CtaKeys = 256;
 constexpr int kQ4MaxSplits = 64;
 
+// Blocks of one batch item of a 4-bit cache, and a block's bytes.
+long long q4_blocks_per_b(int H, int T_max, int D, const uint8_t* dense) {
+  long long n = 0;
+  for (int h = 0; h < H; ++h) n += decode_q4::blocks_of(dense != nullptr && dense[h] != 0 ? T_max : T_max / D);
+  return n;
+}
+size_t q4_block_bytes(int Dh) { return Dh == 128 ? sizeof(decode_q4::Block<128>) : sizeof(decode_q4::Block<64>); }
+
 long long q4_split(int B, int H, int T_max, int D, int W, const uint8_t* head_mask, long long max_keys) {
   const long long slots = (long long)sm_count() * decode_q4::kCtasPerSm;
-  long long best = std::max(max_keys, 1ll), best_cost = 0;
+  long long best = decode_q4::kStep, best_cost = 0;      // splits are whole blocks of slots
   for (int n = 1; n <= kQ4MaxSplits; ++n) {
-    const long long split = (max_keys + n - 1) / n;
+    const long long split = ((max_keys + n - 1) / n + decode_q4::kStep - 1) / decode_q4::kStep * decode_q4::kStep;
     if (n > 1 && split < kQ4CtaKeys) break;
     long long ctas = 0;
     for (int h = 0; h < H; ++h) {
@@ -676,7 +684,7 @@ long long q4_split(int B, int H, int T_max, int D, int W, const uint8_t* head_ma
       ctas += std::max(1ll, (keys + split - 1) / std::max(split, 1ll));
     }
     const long long cost = (ctas * B + slots - 1) / slots * (split + kQ4CtaKeys);
-    if (n == 1 || cost < best_cost) { best = std::max(split, 1ll); best_cost = cost; }
+    if (n == 1 || cost < best_cost) { best = std::max(split, (long long)decode_q4::kStep); best_cost = cost; }
   }
   return best;
 }
@@ -718,19 +726,21 @@ int cache_layout(int B, int H, int Dh, int T_max, int D, int W, const uint8_t* h
   L->split_keys = (int)split;
   L->max_splits = (int)((max_keys + L->split_keys - 1) / L->split_keys);
   if (L->max_splits < 1) L->max_splits = 1;
-  const size_t ring_row = (size_t)Dh * 2, row_bytes = q4 ? (size_t)Dh / 2 : ring_row;
+  const size_t row_bytes = (size_t)Dh * 2;
   size_t off = 0;
   auto take = [&](size_t bytes) { size_t o = off; off += scan::align256(bytes); return o; };
-  L->off_kc = take((size_t)B * per_b * row_bytes);
-  L->off_vc = take((size_t)B * per_b * row_bytes);
-  L->off_kw = take((size_t)B * H * W * ring_row);
-  L->off_vw = take((size_t)B * H * W * ring_row);
+  if (q4) {
+    L->off_kc = take((size_t)B * q4_blocks_per_b(H, T_max, D, head_mask) * q4_block_bytes(Dh));
+    L->off_vc = off;
+  } else {
+    L->off_kc = take((size_t)B * per_b * row_bytes);
+    L->off_vc = take((size_t)B * per_b * row_bytes);
+  }
+  L->off_kw = take((size_t)B * H * W * row_bytes);
+  L->off_vw = take((size_t)B * H * W * row_bytes);
   L->off_len = take((size_t)B * 4);
   L->off_part = take((size_t)B * H * L->max_splits * (Dh + 2) * 4);
   L->off_cnt = take((size_t)(B * H + B) * 4);
-  const size_t par_bytes = q4 ? (size_t)B * per_b * (Dh / decode_q4::kGroup) * 4 : 0;
-  L->off_kp = take(par_bytes);
-  L->off_vp = take(par_bytes);
   L->total = off;
   return RATP_OK;
 }
@@ -756,7 +766,7 @@ int cache_init_common(ratp_cache* c, void* buffer, size_t bytes, int B, int H, i
   char* base = static_cast<char*>(buffer);
   memset(c, 0, sizeof(*c));
   c->Kc = base + L.off_kc;
-  c->Vc = base + L.off_vc;
+  c->Vc = kv_bits == 4 ? nullptr : base + L.off_vc;
   c->Kw = W > 0 ? base + L.off_kw : nullptr;
   c->Vw = W > 0 ? base + L.off_vw : nullptr;
   c->len = reinterpret_cast<int32_t*>(base + L.off_len);
@@ -770,8 +780,6 @@ int cache_init_common(ratp_cache* c, void* buffer, size_t bytes, int B, int H, i
   c->window_L = 0;
   c->in_ring = nullptr;
   c->kv_bits = kv_bits;
-  c->Kp = kv_bits == 4 ? base + L.off_kp : nullptr;
-  c->Vp = kv_bits == 4 ? base + L.off_vp : nullptr;
   for (int h = 0; h < H; ++h) c->dense[h] = (head_mask != nullptr && head_mask[h] != 0) ? 1 : 0;
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   if (cudaMemsetAsync(c->len, 0, (size_t)B * 4, st) != cudaSuccess) return RATP_ERR_CUDA;
@@ -1205,19 +1213,27 @@ int ratp_cache_init_q4(ratp_cache* c, void* buffer, size_t bytes, int B, int H, 
 int ratp_cache_read_q4(const ratp_cache* c, float* k, float* v, void* stream) {
   if (!c || c->kv_bits != 4) return RATP_ERR_ARG;
   if ((k && !aligned16(k)) || (v && !aligned16(v))) return RATP_ERR_ALIGN;
-  const long long quads = (long long)c->B * c->rows_per_b * (c->Dh / 4);
-  const long long grid = (quads + 256 * decode_q4::kReadPer - 1) / (256 * decode_q4::kReadPer);
+  decode_q4::ReadParams p;
+  p.blocks = c->Kc;
+  p.rows_per_b = c->rows_per_b;
+  p.B = c->B; p.H = c->H; p.D = c->D; p.T_max = c->T_max;
+  int rc = read_mask(c->dense, c->H, p.dense_bits, nullptr, nullptr, nullptr, nullptr);
+  if (rc) return rc;
+  if (c->B * q4_blocks_per_b(c->H, c->T_max, c->D, c->dense) > 0x7fffffffll) return RATP_ERR_SHAPE;
+  p.base[0] = 0;
+  for (int h = 0; h < c->H; ++h)
+    p.base[h + 1] = p.base[h] + (int)decode_q4::blocks_of(c->dense[h] ? c->T_max : c->T_max / c->D);
+  const long long grid = (long long)p.base[c->H] * c->B;
   if (grid == 0) return RATP_OK;
-  if (grid > 0x7fffffffll) return RATP_ERR_SHAPE;
   cudaStream_t st = static_cast<cudaStream_t>(stream);
-  const void* codes[2] = {c->Kc, c->Vc};
-  const void* par[2] = {c->Kp, c->Vp};
   float* out[2] = {k, v};
   for (int i = 0; i < 2; ++i) {
     if (out[i] == nullptr) continue;
-    decode_q4::unpack_kernel<<<(unsigned)grid, 256, 0, st>>>(static_cast<const uint32_t*>(codes[i]),
-                                                             static_cast<const uint32_t*>(par[i]), out[i], quads);
-    const int rc = launch_status();
+    p.out = out[i];
+    p.value = i;
+    if (c->Dh == 128) decode_q4::unpack_kernel<128><<<(unsigned)grid, 256, 0, st>>>(p);
+    else decode_q4::unpack_kernel<64><<<(unsigned)grid, 256, 0, st>>>(p);
+    rc = launch_status();
     if (rc) return rc;
   }
   return RATP_OK;
@@ -1252,8 +1268,7 @@ int ratp_cache_pack(ratp_cache* c, const void* hk, const void* hv, int T, void* 
   if (c->kv_bits == 4) {
     decode_q4::PackParams p4;
     p4.d = p;
-    p4.Kp = static_cast<uint32_t*>(c->Kp);
-    p4.Vp = static_cast<uint32_t*>(c->Vp);
+    p4.blocks_per_b = q4_blocks_per_b(c->H, c->T_max, c->D, c->dense);
     p4.base[0] = 0;
     for (int h = 0; h < c->H; ++h) {
       const int rows = T / (c->dense[h] ? 1 : c->D) + (c->W > 0 ? (T < c->W ? T : c->W) : 0);
@@ -1395,10 +1410,9 @@ int decode_launch(const void* q, const void* xk, const void* xv, const void* g,
   if (c->kv_bits == 4) {
     decode_q4::Params p4;
     p4.d = p;
-    p4.Kp = static_cast<uint32_t*>(c->Kp);
-    p4.Vp = static_cast<uint32_t*>(c->Vp);
+    p4.blocks_per_b = q4_blocks_per_b(c->H, c->T_max, c->D, c->dense);
     const int smem = decode_q4::kWarps * decode_q4::kStages *
-                     (int)(c->Dh == 128 ? sizeof(decode_q4::Stage<128>) : sizeof(decode_q4::Stage<64>));
+                     (int)q4_block_bytes(c->Dh);
     cfg.dynamicSmemBytes = smem;
     cfg.blockDim = dim3(decode_q4::kThreads);
     auto kernel = c->Dh == 128 ? decode_q4::decode_kernel<128> : decode_q4::decode_kernel<64>;

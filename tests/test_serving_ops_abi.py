@@ -67,8 +67,9 @@ def test_cache_q4_bytes_and_refusals(lib):
     assert lib.ratp_cache_bytes_q4(B, H, Dh, T, D, W, None, ctypes.byref(n)) == 0
     assert lib.ratp_cache_bytes(B, H, Dh, T, D, W, None, ctypes.byref(m)) == 0
     rows, ring = B * H * (T // D), B * H * W
-    assert n.value >= 2 * (rows * 80 + ring * 256)        # 64 bytes of codes + 16 of parameters; a bf16 ring
-    assert n.value < 2 * (rows * 80 + ring * 256) + m.value - 2 * (rows + ring) * 256 + (1 << 20)
+    held = B * H * (-(-(T // D) // 32) * 32)              # whole blocks of 32 slots
+    assert n.value >= 2 * (held * 80 + ring * 256)        # 64 bytes of codes + 16 of parameters; a bf16 ring
+    assert n.value < 2 * (held * 80 + ring * 256) + m.value - 2 * (rows + ring) * 256 + (1 << 20)
     assert lib.ratp_cache_bytes_q4(1, 4, 96, 64, 4, 0, None, ctypes.byref(n)) == SHAPE
     assert lib.ratp_cache_bytes_q4(1, 4, 128, 64, 0, 0, None, ctypes.byref(n)) == ARG
     assert lib.ratp_cache_bytes_q4(1, 4, 128, 64, 4, -1, None, ctypes.byref(n)) == ARG
@@ -149,8 +150,8 @@ def test_view_and_cache_structs_have_the_c_sizes(tmp_path):
     src = tmp_path / "sizes.c"
     src.write_text('#include <stdio.h>\n#include <stddef.h>\n#include "ratp.h"\n'
                    'int main(void) { printf("%zu %zu %zu %zu\\n", sizeof(ratp_view), offsetof(ratp_view, heads), '
-                   'sizeof(ratp_cache), offsetof(ratp_cache, Kp)); return 0; }\n')
+                   'sizeof(ratp_cache), offsetof(ratp_cache, kv_bits)); return 0; }\n')
     exe = tmp_path / "sizes"
     subprocess.check_call(["gcc", "-std=c99", "-I", os.path.join(ROOT, "include"), str(src), "-o", str(exe)])
     got = [int(x) for x in subprocess.check_output([str(exe)]).split()]
-    assert got == [_binding._VIEW.size, 32, ctypes.sizeof(_binding.CacheStruct), _binding.CacheStruct.Kp.offset]
+    assert got == [_binding._VIEW.size, 32, ctypes.sizeof(_binding.CacheStruct), _binding.CacheStruct.kv_bits.offset]
