@@ -117,48 +117,57 @@ __device__ __forceinline__ uint32_t code_bits(float d, float s, float r) {
 }
 __device__ __forceinline__ int nibble_shift(int c) { return 4 * ((c >> 1) + 4 * (c & 1)); }
 
-// 8 consecutive channels of a row (bf16 pairs) -> one code word; the 4 lanes of
-// a group of 32 channels (consecutive, aligned) share its parameters.  All 4
-// call.  A code is first taken from the quotient's product d r snapped to a
+// 8 M consecutive channels of a row (bf16 pairs) -> M code words; the 4 / M lanes
+// of a group of 32 channels (consecutive, aligned) share its parameters.  All of
+// them call.  A code is first taken from the quotient's product d r snapped to a
 // multiple of 2^-19 (2^-18 past 8) by the first addition, which makes exact
 // ties exact again, and rounded to even by the second; the remainder shows the
-// rare word in which a quotient that near a tie was none (x some 2^18 times
-// smaller than the group's minimum), and that word is done over.
-__device__ __forceinline__ uint32_t quantise8(const uint4& x, uint32_t* par, unsigned lanes) {
-  const uint32_t v[4] = {x.x, x.y, x.z, x.w};
+// rare case of a quotient that near a tie that was none (x some 2^18 times
+// smaller than the group's minimum), and the words are done over.
+template <int M>
+__device__ __forceinline__ void quantise(const uint4* x, uint32_t* words, uint32_t* par, unsigned lanes) {
+  const uint32_t* v = reinterpret_cast<const uint32_t*>(x);
   __nv_bfloat162 lo2 = *reinterpret_cast<const __nv_bfloat162*>(&v[0]), hi2 = lo2;
 #pragma unroll
-  for (int i = 1; i < 4; ++i) {
+  for (int i = 1; i < 4 * M; ++i) {
     const __nv_bfloat162 e = *reinterpret_cast<const __nv_bfloat162*>(&v[i]);
     lo2 = __hmin2(lo2, e);
     hi2 = __hmax2(hi2, e);
   }
   float lo = fminf(__low2float(lo2), __high2float(lo2)), hi = fmaxf(__low2float(hi2), __high2float(hi2));
 #pragma unroll
-  for (int off = 1; off < 4; off <<= 1) {
+  for (int off = 1; off < 4 / M; off <<= 1) {
     lo = fminf(lo, __shfl_xor_sync(lanes, lo, off));
     hi = fmaxf(hi, __shfl_xor_sync(lanes, hi, off));
   }
   *par = group_params(lo, hi);
   const float s = param_scale(*par), m = param_min(*par);
-  if (!(s > 0.f)) return 0u;                   // a constant group
+#pragma unroll
+  for (int j = 0; j < M; ++j) words[j] = 0u;
+  if (!(s > 0.f)) return;                      // a constant group
   const float r0 = __fdividef(1.f, s), r = __fmaf_rn(r0, __fmaf_rn(-s, r0, 1.f), r0);   // 1 / s within 2^-24
-  float f[8];
-  Elem<__nv_bfloat16>::unpack(x, f);
-  uint32_t w = 0;
   float far = 0.f;
 #pragma unroll
-  for (int i = 0; i < 8; ++i) {
-    const float d = __fsub_rn(f[i], m);
-    const float nb = __fadd_rn(__fmaf_rn(d, r, 24.f), kIntBias - 24.f);
-    far = fmaxf(far, fabsf(__fmaf_rn(kIntBias - nb, s, d)));
-    w += (__float_as_uint(nb) - 0x4b400000u) << nibble_shift(i);
-  }
-  if (2.f * far <= s) return w;
-  w = 0;
+  for (int j = 0; j < M; ++j) {
+    float f[8];
+    Elem<__nv_bfloat16>::unpack(x[j], f);
 #pragma unroll
-  for (int i = 0; i < 8; ++i) w |= (code_bits(__fsub_rn(f[i], m), s, r) & 15u) << nibble_shift(i);
-  return w;
+    for (int i = 0; i < 8; ++i) {
+      const float d = __fsub_rn(f[i], m);
+      const float nb = __fadd_rn(__fmaf_rn(d, r, 24.f), kIntBias - 24.f);
+      far = fmaxf(far, fabsf(__fmaf_rn(kIntBias - nb, s, d)));
+      words[j] += (__float_as_uint(nb) - 0x4b400000u) << nibble_shift(i);
+    }
+  }
+  if (2.f * far <= s) return;
+#pragma unroll
+  for (int j = 0; j < M; ++j) {
+    float f[8];
+    Elem<__nv_bfloat16>::unpack(x[j], f);
+    words[j] = 0u;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) words[j] |= (code_bits(__fsub_rn(f[i], m), s, r) & 15u) << nibble_shift(i);
+  }
 }
 
 // ---- prefill -> cache hand-off ------------------------------------------------
@@ -178,17 +187,17 @@ __device__ __forceinline__ int head_at(const int* base, int H, int at) {
   return lo;
 }
 
-// Dh/8 threads per row, kPackRows rows per thread; a block holds rows of one
+// Dh/16 threads per row, kPackRows rows per thread; a block holds rows of one
 // (b, h): its dilated rows first (quantised), then its ring rows (copied).
 // Heads take blocks as they need (base[h]): a dense head has D times a dilated
 // one's rows.  A thread has all its rows' loads in flight at once, and the
-// block's index arithmetic is spread over them.
-constexpr int kPackRows = 4;
+// block's index arithmetic and a group's parameters are spread over 16 channels.
+constexpr int kPackRows = 2;
 template <int DH>
 __global__ void __launch_bounds__(256)
 pack_kernel(const __grid_constant__ PackParams pp) {
   const decode::PackParams& p = pp.d;
-  constexpr int TPR = DH / 8;
+  constexpr int TPR = DH / 16;
   constexpr int RPB = 256 / TPR;
   const int b = blockIdx.x / pp.base[p.H], at = blockIdx.x - b * pp.base[p.H];
   const int h = head_at(pp.base, p.H, at);
@@ -200,42 +209,47 @@ pack_kernel(const __grid_constant__ PackParams pp) {
   const int w_lo = max(0, p.T - p.W);
   const int n_ring = (p.W > 0) ? (p.T - w_lo) : 0;
   if (at == 0 && threadIdx.x == 0) p.len[b] = p.T;
-  const long long src_base = (long long)b * p.T * p.H * DH + (long long)h * DH + li * 8;
+  const long long src_base = (long long)b * p.T * p.H * DH + (long long)h * DH + li * 16;
   [[maybe_unused]] const long long n_src = (long long)p.B * p.T * p.H * DH;
   const long long block0 = (long long)b * pp.blocks_per_b + head_block(p.dense_bits, h, p.T_max, p.D);
   Block<DH>* const blocks = reinterpret_cast<Block<DH>*>(p.Kc) + block0;
-  const unsigned lanes = 0xfu << ((threadIdx.x & 31) & ~3);
+  const unsigned lanes = 0x3u << ((threadIdx.x & 31) & ~1);
 
-  uint4 in[kPackRows][2];
+  uint4 in[kPackRows][2][2];
 #pragma unroll
   for (int i = 0; i < kPackRows; ++i) {
     const int r = r0 + i * RPB;
     const int pos = r < n_dil ? r * Dd + Dd - 1 : w_lo + (r - n_dil);
     const long long src = src_base + (long long)pos * p.H * DH;
-    in[i][0] = in[i][1] = make_uint4(0u, 0u, 0u, 0u);
-    if (r < n_dil + n_ring && RATP_IN(src, 8, n_src)) {
-      in[i][0] = __ldcs(reinterpret_cast<const uint4*>(p.hk + src));
-      in[i][1] = __ldcs(reinterpret_cast<const uint4*>(p.hv + src));
-    }
+    const bool there = r < n_dil + n_ring && RATP_IN(src, 16, n_src);
+#pragma unroll
+    for (int s = 0; s < 2; ++s)
+#pragma unroll
+      for (int j = 0; j < 2; ++j)
+        in[i][s][j] = there ? __ldcs(reinterpret_cast<const uint4*>((s == 0 ? p.hk : p.hv) + src) + j)
+                            : make_uint4(0u, 0u, 0u, 0u);
   }
 #pragma unroll
   for (int i = 0; i < kPackRows; ++i) {
-    const int r = r0 + i * RPB;                // the same for a group's 4 lanes
+    const int r = r0 + i * RPB;                // the same for a group's 2 lanes
     if (r < n_dil) {
       if (!RATP_IN(block0 + r / kStep, 1, p.B * pp.blocks_per_b)) continue;
       Block<DH>& blk = blocks[r / kStep];
 #pragma unroll
       for (int s = 0; s < 2; ++s) {
-        uint32_t par;
-        const uint32_t w = quantise8(in[i][s], &par, lanes);
-        (s == 0 ? blk.k : blk.v)[r % kStep][li] = w;
-        if ((li & 3) == 0) (s == 0 ? blk.kp : blk.vp)[r % kStep][li / 4] = par;
+        uint32_t par, w[2];
+        quantise<2>(in[i][s], w, &par, lanes);
+        *reinterpret_cast<uint2*>(&(s == 0 ? blk.k : blk.v)[r % kStep][2 * li]) = make_uint2(w[0], w[1]);
+        if ((li & 1) == 0) (s == 0 ? blk.kp : blk.vp)[r % kStep][li / 2] = par;
       }
     } else if (r < n_dil + n_ring) {
-      const long long dst = (((long long)b * p.H + h) * p.W + (w_lo + (r - n_dil)) % p.W) * DH + li * 8;
-      if (!RATP_IN(dst, 8, (long long)p.B * p.H * p.W * DH)) continue;
-      *reinterpret_cast<uint4*>(p.Kw + dst) = in[i][0];
-      *reinterpret_cast<uint4*>(p.Vw + dst) = in[i][1];
+      const long long dst = (((long long)b * p.H + h) * p.W + (w_lo + (r - n_dil)) % p.W) * DH + li * 16;
+      if (!RATP_IN(dst, 16, (long long)p.B * p.H * p.W * DH)) continue;
+#pragma unroll
+      for (int j = 0; j < 2; ++j) {
+        reinterpret_cast<uint4*>(p.Kw + dst)[j] = in[i][0][j];
+        reinterpret_cast<uint4*>(p.Vw + dst)[j] = in[i][1][j];
+      }
     }
   }
 }
@@ -661,7 +675,9 @@ decode_kernel(const Params pp) {
           float2 f[4];
 #pragma unroll
           for (int i = 0; i < 4; ++i) f[i] = *reinterpret_cast<const float2*>(&s_self[st][8 * w + 2 * i]);
-          const uint32_t code = quantise8(Elem<__nv_bfloat16>::pack2(f), &par, 0xfu << (lane & ~3));
+          const uint4 x = Elem<__nv_bfloat16>::pack2(f);
+          uint32_t code;
+          quantise<1>(&x, &code, &par, 0xfu << (lane & ~3));
           Block<DH>& blk = blocks[app_slot / kStep];
           (st == 0 ? blk.k : blk.v)[app_slot % kStep][w] = code;
           if ((w & 3) == 0) (st == 0 ? blk.kp : blk.vp)[app_slot % kStep][w / 4] = par;

@@ -1272,7 +1272,7 @@ int ratp_cache_pack(ratp_cache* c, const void* hk, const void* hv, int T, void* 
     p4.base[0] = 0;
     for (int h = 0; h < c->H; ++h) {
       const int rows = T / (c->dense[h] ? 1 : c->D) + (c->W > 0 ? (T < c->W ? T : c->W) : 0);
-      const int per = rpb * decode_q4::kPackRows;
+      const int per = 256 / (c->Dh / 16) * decode_q4::kPackRows;
       p4.base[h + 1] = p4.base[h] + (rows + per - 1) / per;
     }
     if (p4.base[c->H] == 0) p4.base[c->H] = 1;   // still sets len
