@@ -65,6 +65,19 @@ __device__ __forceinline__ float decay_power(float log_decay, double n) {
   return n == 0.0 ? 1.f : (float)exp(fmax((double)log_decay, -1.0e4) * n);
 }
 
+// The same to twice the bits, for what a state is multiplied by again and again:
+// a rounding of the power alone would drift the state by as many of its roundings
+// as there are chunks (or decode tokens) within the decay's reach.
+struct Decay {
+  float hi, lo;
+  __device__ __forceinline__ float step(float s, float add) const { return fmaf(hi, s, fmaf(lo, s, add)); }
+};
+__device__ __forceinline__ Decay decay_pair(float log_decay, double n) {
+  const double x = n == 0.0 ? 1.0 : exp(fmax((double)log_decay, -1.0e4) * n);
+  const float hi = (float)x;
+  return {hi, (float)(x - (double)hi)};
+}
+
 template <int DH>
 struct Layout {
   static constexpr uint32_t kHalf = C * 128;             // 128 rows x 64 bf16
@@ -73,7 +86,8 @@ struct Layout {
   static constexpr uint32_t kOffS = kOffO + kTile;       // S, bf16 [DH / 64][DH rows][64]
   static constexpr uint32_t kSHalf = DH * 128;
   static constexpr uint32_t kOffPow = kOffS + (DH / 64) * kSHalf;    // a^0 .. a^128
-  static constexpr uint32_t kOffBar = kOffPow + (C + 1) * 4 + 4;
+  static constexpr uint32_t kOffDecay = kOffPow + (C + 2) * 4;       // of a whole chunk, of the sequence's last
+  static constexpr uint32_t kOffBar = kOffDecay + 2 * sizeof(Decay);
   static constexpr int kBars = 2 * kSlots + 15;
   static constexpr uint32_t kOffCtl = kOffBar + kBars * 8;           // TMEM address, abort flag
   // one CTA per SM whatever DH, since each takes all of TMEM
@@ -150,6 +164,7 @@ chunk_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ C
   const uint32_t b_pd = b_qk + 80, b_sf = b_qk + 96;
   const uint32_t b_qs = b_qk + 112;                      // Q S done
   float* s_pow = reinterpret_cast<float*>(smem + L::kOffPow);
+  Decay* s_decay = reinterpret_cast<Decay*>(smem + L::kOffDecay);
   uint32_t* s_tmem = reinterpret_cast<uint32_t*>(smem + L::kOffCtl);
   volatile int* s_abort = reinterpret_cast<volatile int*>(smem + L::kOffCtl + 4);
   const int warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;   // warp: known uniform
@@ -194,6 +209,8 @@ chunk_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ C
   }
   const float ld = p.log_decay[h];
   if (threadIdx.x <= C) s_pow[threadIdx.x] = decay_power(ld, (double)threadIdx.x);
+  else if (threadIdx.x <= C + 2)
+    s_decay[threadIdx.x - C - 1] = decay_pair(ld, threadIdx.x == C + 1 ? (double)C : (double)(p.T - (p.n_chunks - 1) * C));
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
@@ -538,7 +555,7 @@ chunk_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ C
     // S = a^n S + chunk c's products, which are done
     auto update = [&](int c) {
       tc_fence_after();
-      const float a = s_pow[tokens(c)];
+      const Decay a = s_decay[tokens(c) == C ? 0 : 1];
       const uint32_t tc = tl + (OUT ? kColS : (uint32_t)(c & 1) * 128u);
       if (mine) {
 #pragma unroll
@@ -547,7 +564,7 @@ chunk_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ C
           tmem_ld32(tc + 32 * q, v);
           tmem_wait_ld();
 #pragma unroll
-          for (int x = 0; x < 32; ++x) S[32 * q + x] = fmaf(a, S[32 * q + x], __uint_as_float(v[x]));
+          for (int x = 0; x < 32; ++x) S[32 * q + x] = a.step(S[32 * q + x], __uint_as_float(v[x]));
         }
       }
       tc_fence_before();
@@ -602,7 +619,7 @@ combine_kernel(float* __restrict__ ws, const float* __restrict__ init, const flo
                int h0, int n_seg, int quads, int seg_tokens, [[maybe_unused]] long long n_ws) {
   const int e = blockIdx.x * 256 + threadIdx.x, pair = blockIdx.y;
   if (e >= quads) return;
-  const float a = decay_power(log_decay[(h0 + pair) % H], (double)seg_tokens);
+  const Decay a = decay_pair(log_decay[(h0 + pair) % H], (double)seg_tokens);
   float4* w = reinterpret_cast<float4*>(ws) + (long long)pair * n_seg * quads + e;
   if (!RATP_IN(((long long)pair * n_seg * quads + e) * 4, ((long long)(n_seg - 1) * quads + 1) * 4, n_ws)) return;
   float4 run = init != nullptr ? reinterpret_cast<const float4*>(init)[(long long)pair * quads + e]
@@ -617,10 +634,10 @@ combine_kernel(float* __restrict__ ws, const float* __restrict__ init, const flo
     for (int i = 0; i < kBatch; ++i) {
       if (s0 + i >= n_seg) break;
       w[(long long)(s0 + i) * quads] = run;
-      run.x = fmaf(a, run.x, own[i].x);
-      run.y = fmaf(a, run.y, own[i].y);
-      run.z = fmaf(a, run.z, own[i].z);
-      run.w = fmaf(a, run.w, own[i].w);
+      run.x = a.step(run.x, own[i].x);
+      run.y = a.step(run.y, own[i].y);
+      run.z = a.step(run.z, own[i].z);
+      run.w = a.step(run.w, own[i].w);
     }
   }
 }
@@ -659,7 +676,7 @@ recurrent_kernel(const RecurrentParams p) {
     S[i] = p.init != nullptr && RATP_IN(at, 4, n_s) ? __ldcs(reinterpret_cast<const float4*>(p.init + at))
                                                     : make_float4(0.f, 0.f, 0.f, 0.f);
   }
-  const float a = decay_power(p.log_decay[h], 1.0);
+  const Decay a = decay_pair(p.log_decay[h], 1.0);
   for (int t = 0; t < p.T; ++t) {
     const long long row = (((long long)b * p.T + t) * p.H + h) * DH;
     const bool in = RATP_IN(row, DH, n_tok);
@@ -677,10 +694,10 @@ recurrent_kernel(const RecurrentParams p) {
 #pragma unroll
     for (int i = 0; i < kRows; ++i) {
       const float k = s_k[g + 16 * i], q = s_q[g + 16 * i];
-      S[i].x = fmaf(a, S[i].x, k * v[0]);
-      S[i].y = fmaf(a, S[i].y, k * v[1]);
-      S[i].z = fmaf(a, S[i].z, k * v[2]);
-      S[i].w = fmaf(a, S[i].w, k * v[3]);
+      S[i].x = a.step(S[i].x, k * v[0]);
+      S[i].y = a.step(S[i].y, k * v[1]);
+      S[i].z = a.step(S[i].z, k * v[2]);
+      S[i].w = a.step(S[i].w, k * v[3]);
       o.x = fmaf(q, S[i].x, o.x);
       o.y = fmaf(q, S[i].y, o.y);
       o.z = fmaf(q, S[i].z, o.z);
