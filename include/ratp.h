@@ -346,8 +346,8 @@ int ratp_dilated_attn_prefill_per_sample_ws(const void* q, const void* hk, const
  * positions: NULL (token t sits at position t); int32 [B] (position of token
  *   0 of each sequence, e.g. a cache's len: token t sits at positions[b] + t);
  *   or int32 [B][T] with positions_per_token != 0.  Any int32 value.
- * Errors: ARG (null pointer, negative size or stride, bad dtype, eps < 0 or
- *   not finite), SHAPE (Dh not 64/128, rot not a multiple of 16 in 0..Dh, too
+ * Errors: ARG (null pointer, negative size or stride, an output whose own rows
+ *   overlap, bad dtype, eps < 0 or not finite), SHAPE (Dh not 64/128, rot not a multiple of 16 in 0..Dh, too
  *   many heads), ALIGN.  B or T == 0 is a no-op.
  * ---------------------------------------------------------------------- */
 typedef struct ratp_view {
@@ -370,7 +370,11 @@ int ratp_qk_norm_rope(const ratp_view* q, const ratp_view* k, const ratp_view* q
  *   o_t = scale * q_t S_t
  *
  * q, k, v, o: bf16 [B][T][H][Dh] (step: [B][H][Dh]), Dh 64 or 128.
- * log_decay: fp32 [H], values <= 0 (0: no decay; -inf: no memory).
+ *   o overlaps none of the others.
+ * log_decay: fp32 [H], values <= 0 (0: no decay; -inf: no memory); a kernel
+ *   that reads another value or a NaN records ARG (ratp_last_error).
+ * A value of v that is not finite makes its channel of o NaN from its token on,
+ *   as one of k does for all channels; tokens before it are as without it.
  * initial_state: fp32 [B][H][Dh][Dh] (row: channel of k, column: channel of v)
  *   before the first token; NULL = zero.  final_state: the state after the
  *   last token, or NULL; it may be initial_state itself (in place).  A prefill
@@ -384,8 +388,8 @@ int ratp_qk_norm_rope(const ratp_view* q, const ratp_view* k, const ratp_view* q
  * ratp_linear_attn_step: one token per sequence, state updated in place.
  * Errors: ARG (null pointer, negative size, scale not finite), SHAPE (Dh, H *
  *   B * tokens too large), ALIGN, CAPACITY (workspace too small), UNSUPPORTED
- *   (dtype not bf16).  B, T or H == 0 is a no-op (final_state is then left as
- *   it is).
+ *   (dtype not bf16).  B or H == 0 is a no-op; T == 0 hands the initial state
+ *   on to final_state.
  * ---------------------------------------------------------------------- */
 int ratp_linear_attn_workspace_bytes(int B, int T, int H, int Dh, size_t* bytes);
 int ratp_linear_attn_prefill(const void* q, const void* k, const void* v, const float* log_decay,
@@ -458,8 +462,8 @@ int ratp_cache_init(ratp_cache* c, void* buffer, size_t bytes,
  * word is s (bf16, low half) and m (bf16, high half).  The window ring stays
  * bf16 and the recurrent state fp32, so the last W positions are read as they
  * are.
- * Values must be finite, max - m within fp32, and a step s below fp32's normal
- * range counts as 0.
+ * A group with a NaN or an infinity, or whose max - m passes fp32, stands for
+ * NaN; a step s below fp32's normal range counts as 0.
  * Every other entry point takes such a cache as it takes a bf16 one
  * (ratp_cache_pack quantises; ratp_decode_step quantises the row it appends
  * and attends to the held values; ratp_decode_step_layers mixes both kinds).

@@ -532,9 +532,13 @@ def qk_norm_rope(q, k, q_weight, k_weight, inv_freq, positions=None, eps=1e-6, i
 def _linear_args(q, k, v, log_decay, states, out, dims):
     if not isinstance(q, torch.Tensor) or q.dim() != dims:
         raise ValueError("q must be a CUDA tensor of %d dimensions" % dims)
+    sh, dev = q.shape, q.get_device()
     if out is None:
         out = torch.empty_like(q)
-    sh, dev = q.shape, q.get_device()
+    elif isinstance(out, torch.Tensor):
+        n, at = 2 * q.numel(), out.data_ptr()
+        if n and any(isinstance(t, torch.Tensor) and abs(t.data_ptr() - at) < n for t in (q, k, v)):
+            raise ValueError("out must not overlap q, k or v")
     for t, nm in ((q, "q"), (k, "k"), (v, "v"), (out, "out")):
         _need(t, nm, torch.bfloat16)
         if t.shape != sh or t.get_device() != dev:
@@ -559,6 +563,7 @@ def linear_attn_prefill(q, k, v, log_decay, initial_state=None, final_state=None
     log_decay: fp32 [H], <= 0.  initial_state: fp32 [B, H, Dh, Dh] before the
     first token (None: zero); final_state: receives the state after the last
     one, and may be initial_state itself.  scale: Dh ** -0.5 by default.
+    out: must not overlap q, k or v.
     workspace: uint8 tensor of ``linear_attn_workspace_bytes`` (default: one
     from the current stream's allocator, so that no two calls or captured
     graphs share one)."""
@@ -569,6 +574,10 @@ def linear_attn_prefill(q, k, v, log_decay, initial_state=None, final_state=None
         if workspace is None:
             n = linear_attn_workspace_bytes(B, T, H, Dh)
             workspace = torch.empty(n, dtype=torch.uint8, device=q.device) if n else None
+        else:
+            _need(workspace, "workspace", torch.uint8)
+            if workspace.get_device() != q.get_device():
+                raise ValueError("workspace must be on the device of q")
         _check("ratp_linear_attn_prefill", lib.ratp_linear_attn_prefill(
             q.data_ptr(), k.data_ptr(), v.data_ptr(), log_decay.data_ptr(), _addr(initial_state), _addr(final_state),
             out.data_ptr(), B, T, H, Dh, Dh ** -0.5 if scale is None else scale, RATP_BF16, _addr(workspace),
@@ -699,10 +708,27 @@ class KVCache:
             off += cap
         raise IndexError(h)
 
+    def _here(self, t, name, numel, whole=True):
+        """``t`` has the elements that a call reads of it, on the cache's device."""
+        n = t.numel()
+        if n < numel or (whole and n != numel) or t.get_device() != self.buffer.get_device():
+            raise ValueError("%s: %s on %s does not fit the cache (B %d, H %d, Dh %d) on %s" % (
+                name, tuple(t.shape), t.device, self.B, self.H, self.Dh, self.buffer.device))
+
+    def _step_args(self, q, xk, xv, g, state, out):
+        n = self.B * self.H * self.Dh
+        for t, nm in ((q, "q"), (xk, "xk"), (xv, "xv"), (g, "g"), (out, "out")):
+            _need(t, nm, torch.bfloat16)
+            self._here(t, nm, n)
+        _need(state, "state", torch.float32)
+        self._here(state, "state", 2 * n)
+
     def pack(self, hk, hv, T=None):
         _need(hk, "hk", torch.bfloat16)
         _need(hv, "hv", torch.bfloat16)
         T = hk.shape[1] if T is None else T
+        for t, nm in ((hk, "hk"), (hv, "hv")):
+            self._here(t, nm, self.B * int(T) * self.H * self.Dh, whole=False)
         with _on(hk.get_device()):
             _check("ratp_cache_pack", load_library().ratp_cache_pack(
                 self._ref, _ptr(hk), _ptr(hv), int(T), _stream(hk)))
@@ -728,12 +754,9 @@ class KVCache:
 
     def decode_step(self, q, xk, xv, g, state, out=None):
         """One token per sequence; state: fp32 [2, B, H, Dh] updated in place."""
-        for t, n in ((q, "q"), (xk, "xk"), (xv, "xv"), (g, "g")):
-            _need(t, n, torch.bfloat16)
-        _need(state, "state", torch.float32)
-        if out is None:
+        if out is None and isinstance(q, torch.Tensor):
             out = torch.empty_like(q)
-        _need(out, "out", torch.bfloat16)
+        self._step_args(q, xk, xv, g, state, out)
         with _on(q.get_device()):
             _check("ratp_decode_step", load_library().ratp_decode_step(
                 q.data_ptr(), xk.data_ptr(), xv.data_ptr(), g.data_ptr(), state.data_ptr(), self._ref, out.data_ptr(),
@@ -752,13 +775,16 @@ def decode_step_layers(layers):
     n = len(layers)
     arr = (DecodeLayerStruct * max(n, 1))()
     for i, (cache, q, xk, xv, g, state, out) in enumerate(layers):
-        for t, nm in ((q, "q"), (xk, "xk"), (xv, "xv"), (g, "g"), (out, "out")):
-            _need(t, nm, torch.bfloat16)
-        _need(state, "state", torch.float32)
+        cache._step_args(q, xk, xv, g, state, out)
         arr[i] = DecodeLayerStruct(q.data_ptr(), xk.data_ptr(), xv.data_ptr(), g.data_ptr(),
                                    state.data_ptr(), ctypes.pointer(cache.c), out.data_ptr())
-    stream = _stream(layers[0][1]) if n else None
-    _check("ratp_decode_step_layers", load_library().ratp_decode_step_layers(arr, n, stream))
+        if q.get_device() != layers[0][1].get_device():
+            raise ValueError("the layers of one call must be on one device")
+    if n == 0:
+        _check("ratp_decode_step_layers", load_library().ratp_decode_step_layers(arr, 0, None))
+        return
+    with _on(layers[0][1].get_device()):
+        _check("ratp_decode_step_layers", load_library().ratp_decode_step_layers(arr, n, _stream(layers[0][1])))
 
 
 def guard_line():

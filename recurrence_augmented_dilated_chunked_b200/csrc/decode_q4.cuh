@@ -96,6 +96,7 @@ __device__ __forceinline__ uint32_t group_params(float lo, float hi) {
   // d / 15 correctly rounded: the product's remainder is exact in one fma, and
   // no quotient by 15 lies near enough to a rounding boundary to be missed
   const float d = __fsub_rn(hi, lo), q = __fmul_rn(d, 1.f / 15.f);
+  if (!(d < INFINITY)) return 0x7fff7fffu;           // a value that is not finite: the group stands for NaN
   const __nv_bfloat16 s = __float2bfloat16_rn(__fmaf_rn(__fmaf_rn(-15.f, q, d), 1.f / 15.f, q));
   const __nv_bfloat16 m = __float2bfloat16_rn(lo);   // exact: lo is a bf16 value
   return (uint32_t)__bfloat16_as_ushort(s) | ((uint32_t)__bfloat16_as_ushort(m) << 16);
@@ -131,20 +132,20 @@ __device__ __forceinline__ void quantise(const uint4* x, uint32_t* words, uint32
 #pragma unroll
   for (int i = 1; i < 4 * M; ++i) {
     const __nv_bfloat162 e = *reinterpret_cast<const __nv_bfloat162*>(&v[i]);
-    lo2 = __hmin2(lo2, e);
-    hi2 = __hmax2(hi2, e);
+    lo2 = __hmin2_nan(lo2, e);
+    hi2 = __hmax2_nan(hi2, e);
   }
-  float lo = fminf(__low2float(lo2), __high2float(lo2)), hi = fmaxf(__low2float(hi2), __high2float(hi2));
 #pragma unroll
   for (int off = 1; off < 4 / M; off <<= 1) {
-    lo = fminf(lo, __shfl_xor_sync(lanes, lo, off));
-    hi = fmaxf(hi, __shfl_xor_sync(lanes, hi, off));
+    lo2 = __hmin2_nan(lo2, __shfl_xor_sync(lanes, lo2, off));
+    hi2 = __hmax2_nan(hi2, __shfl_xor_sync(lanes, hi2, off));
   }
-  *par = group_params(lo, hi);
+  *par = group_params(__bfloat162float(__hmin_nan(__low2bfloat16(lo2), __high2bfloat16(lo2))),
+                      __bfloat162float(__hmax_nan(__low2bfloat16(hi2), __high2bfloat16(hi2))));
   const float s = param_scale(*par), m = param_min(*par);
 #pragma unroll
   for (int j = 0; j < M; ++j) words[j] = 0u;
-  if (!(s > 0.f)) return;                      // a constant group
+  if (!(s > 0.f)) return;                      // a constant group, or NaN
   const float r0 = __fdividef(1.f, s), r = __fmaf_rn(r0, __fmaf_rn(-s, r0, 1.f), r0);   // 1 / s within 2^-24
   float far = 0.f;
 #pragma unroll

@@ -28,7 +28,7 @@
 // segment's own state (from zero), combine_kernel turns those into the state
 // before each segment, and chunk_kernel<DH, true> runs all segments at once.
 //
-// Roles of chunk_kernel (448 threads, one CTA per SM):
+// Roles of chunk_kernel (512 threads, one CTA per SM):
 //   warps 0-3   P: read Q K^T from TMEM, mask, decay, write bf16 P to TMEM over
 //               it; then o = scale a^{i+1} O1 + O2 out of TMEM to memory;
 //   warps 4-11  state, half of its columns to each four warps: scale K in place
@@ -40,6 +40,7 @@
 //               O1 = Q S, O2 = P V, SL = K'^T V (M = Dh).  Q K^T of the next
 //               chunk goes between the first and the other parts of SL, so that
 //               P of the next chunk is worked out while this one's state is.
+//   warps 14, 15  keep values that are not finite out of the outputs before them.
 //   Without an output (<DH, false>) only SL is computed, in two buffers, and
 //   warps 0-3 share the scaling of K.
 // Bound: 4 tiles of memory traffic per chunk and (b, h) against six products.
@@ -50,20 +51,22 @@ namespace ratp {
 namespace linear_attn {
 
 constexpr int C = 128;                 // tokens per chunk
-constexpr int kThreads = 448;
+constexpr int kThreads = 512;
 constexpr int kStateWarps = 8;         // warps 4 .. 11
 constexpr int kProducerWarp = 12;
 constexpr int kMmaWarp = 13;
+constexpr int kScanWarp = 14;          // and 15
 constexpr int kSlots = 5;
 constexpr int kPart = 32;               // tokens whose scaled K is handed to the MMA at a time
 constexpr int kParts = C / kPart;
 constexpr int kRecurrentTokens = 16;
 
 // a^n for n >= 0 tokens.  log_decay is clamped to a finite value, below which
-// every power but the 0th is zero in fp32.
-__device__ __forceinline__ float decay_power(float log_decay, double n) {
-  return n == 0.0 ? 1.f : (float)exp(fmax((double)log_decay, -1.0e4) * n);
+// every power but the 0th is zero in fp32 (a NaN stays one).
+__device__ __forceinline__ double exact_power(float log_decay, double n) {
+  return n == 0.0 ? 1.0 : exp((log_decay < -1.0e4f ? -1.0e4 : (double)log_decay) * n);
 }
+__device__ __forceinline__ float decay_power(float log_decay, double n) { return (float)exact_power(log_decay, n); }
 
 // The same to twice the bits, for what a state is multiplied by again and again:
 // a rounding of the power alone would drift the state by as many of its roundings
@@ -73,7 +76,7 @@ struct Decay {
   __device__ __forceinline__ float step(float s, float add) const { return fmaf(hi, s, fmaf(lo, s, add)); }
 };
 __device__ __forceinline__ Decay decay_pair(float log_decay, double n) {
-  const double x = n == 0.0 ? 1.0 : exp(fmax((double)log_decay, -1.0e4) * n);
+  const double x = exact_power(log_decay, n);
   const float hi = (float)x;
   return {hi, (float)(x - (double)hi)};
 }
@@ -88,10 +91,12 @@ struct Layout {
   static constexpr uint32_t kOffPow = kOffS + (DH / 64) * kSHalf;    // a^0 .. a^128
   static constexpr uint32_t kOffDecay = kOffPow + (C + 2) * 4;       // of a whole chunk, of the sequence's last
   static constexpr uint32_t kOffBar = kOffDecay + 2 * sizeof(Decay);
-  static constexpr int kBars = 2 * kSlots + 15;
-  static constexpr uint32_t kOffCtl = kOffBar + kBars * 8;           // TMEM address, abort flag
+  static constexpr int kBars = 2 * kSlots + 17;
+  static constexpr uint32_t kOffCtl = kOffBar + kBars * 8;           // TMEM address, abort flag, bad[2]
+  static constexpr uint32_t kOffFirst = kOffCtl + 16;                // first[2][DH], bytes
   // one CTA per SM whatever DH, since each takes all of TMEM
-  static constexpr uint32_t kBytes = (kOffCtl + 8 + 1024) > 120 * 1024 ? (kOffCtl + 8 + 1024) : 120 * 1024;
+  static constexpr uint32_t kUsed = kOffFirst + 2 * DH + 1024;
+  static constexpr uint32_t kBytes = kUsed > 120 * 1024 ? kUsed : 120 * 1024;
 };
 static_assert(Layout<128>::kBytes <= 232448, "shared memory of one CTA");
 
@@ -163,10 +168,13 @@ chunk_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ C
   // barriers [c & 1], phase c / 2
   const uint32_t b_pd = b_qk + 80, b_sf = b_qk + 96;
   const uint32_t b_qs = b_qk + 112;                      // Q S done
+  const uint32_t b_vs = b_qk + 120;                      // [2]: V of chunk c is finite, barrier [c & 1]
   float* s_pow = reinterpret_cast<float*>(smem + L::kOffPow);
   Decay* s_decay = reinterpret_cast<Decay*>(smem + L::kOffDecay);
   uint32_t* s_tmem = reinterpret_cast<uint32_t*>(smem + L::kOffCtl);
   volatile int* s_abort = reinterpret_cast<volatile int*>(smem + L::kOffCtl + 4);
+  int* s_bad = reinterpret_cast<int*>(smem + L::kOffCtl + 8);        // [c & 1]: V of chunk c was not finite,
+  uint8_t* s_first = smem + L::kOffFirst;                            // column x from token s_first[c & 1][x] on
   const int warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;   // warp: known uniform
 
   // segment `seg` of (b, h)
@@ -198,6 +206,7 @@ chunk_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ C
       mbar_init(b_kv + 8 * i, 1);
       mbar_init(b_pd + 8 * i, 1);
       mbar_init(b_sf + 8 * i, 32 * kStateWarps);
+      mbar_init(b_vs + 8 * i, 64);
     }
     mbar_init(b_s, 32 * kStateWarps);
     mbar_init(b_final, 1);
@@ -208,6 +217,7 @@ chunk_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ C
     tmem_relinquish();
   }
   const float ld = p.log_decay[h];
+  if (!(ld <= 0.f) && seg == 0 && threadIdx.x == 0) raise_error(RATP_ERR_ARG);
   if (threadIdx.x <= C) s_pow[threadIdx.x] = decay_power(ld, (double)threadIdx.x);
   else if (threadIdx.x <= C + 2)
     s_decay[threadIdx.x - C - 1] = decay_pair(ld, threadIdx.x == C + 1 ? (double)C : (double)(p.T - (p.n_chunks - 1) * C));
@@ -377,12 +387,16 @@ chunk_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ C
         __syncwarp();
       }
       if (!ok) break;
+      if (c < n_state && elect_one()) umma_commit(b_pd + 8 * (c & 1));
+      __syncwarp();
       // P is there and O holds the scaled Q S.  These products and the next
       // chunk's Q K^T run while the state warps bring S forward.
-      if (OUT && !warp_all(mbar_wait(b_p, par, s_abort))) { ok = false; break; }
+      if (OUT && !warp_all(mbar_wait(b_p, par, s_abort) && mbar_wait(b_vs + 8 * (c & 1), (uint32_t)(c >> 1) & 1u, s_abort))) {
+        ok = false;
+        break;
+      }
       tc_fence_after();
       if (elect_one()) {
-        if (c < n_state) umma_commit(b_pd + 8 * (c & 1));
         if (OUT) {
 #pragma unroll
           for (int k = 0; k < C / 16; ++k)
@@ -412,7 +426,7 @@ chunk_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ C
       const float ai = s_pow[i + 1] * p.scale;
       // (a decay below 2^-160 a token is none of it: a^1 is zero in fp32 either
       // way, and the bound keeps the exponents' rounding below P's)
-      const float l2a = fmaxf(ld * 1.4426950408889634f, -160.f);
+      const float l2a = ld < -110.f ? -160.f : ld * 1.4426950408889634f;
       const float top = log2f(fabsf(p.scale));           // on the diagonal: |scale| 2^(l2a (i - j)), at most |scale|
       const float base = fmaf(l2a, (float)lane, top);
       const uint32_t flip = p.scale < 0.f ? 0x80008000u : 0u;
@@ -478,11 +492,17 @@ chunk_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ C
       // o through a staging tile, so that a copy writes whole rows
       auto work_o = [&](int c) {
         tc_fence_after();
+        const bool bad = s_bad[c & 1] != 0;
 #pragma unroll 2
         for (int q = 0; q < DH / 32; ++q) {
           uint32_t r[32];
           tmem_ld32(tl + kColO + 32 * q, r);
           tmem_wait_ld();
+          if (bad) {                                     // the columns of V that were not finite, from their token on
+#pragma unroll
+            for (int x = 0; x < 32; ++x)
+              if (s_first[(c & 1) * DH + 32 * q + x] <= i) r[x] = 0x7fffffffu;
+          }
           if (q + 1 == DH / 32) {
             tc_fence_before();
             mbar_arrive(b_ofree);                        // O is read
@@ -507,7 +527,8 @@ chunk_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ C
         }
       };
       for (int c = 0; c < n; ++c) {
-        const bool there = work_p(c) && warp_all(mbar_wait(b_o, (uint32_t)c & 1u, s_abort));
+        const bool there = work_p(c) && warp_all(mbar_wait(b_o, (uint32_t)c & 1u, s_abort) &&
+                                                 mbar_wait(b_vs + 8 * (c & 1), (uint32_t)(c >> 1) & 1u, s_abort));
         // the copy of the chunk before has read the staging tile; the four warps
         // go on, or give up, together
         if (threadIdx.x == 0) asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory");
@@ -519,6 +540,46 @@ chunk_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ C
       // parts 0 and 2; the state warps' second half has 1 and 3
       for (int c = 0; c < n; ++c)
         if (!warp_all(full_wait(c * kUnits + kK)) || !scale_k(c, 0, 2)) break;
+    }
+  } else if (warp >= kScanWarp) {
+    // ------------------------------------------------------------ scan of V
+    // P V multiplies the values of the tokens after i by zeros, so that one which
+    // is not finite would reach the outputs before it.  Where a tile has any, they
+    // are made zeros once the state's products have read them, and the outputs
+    // from their token on are made NaN, as the state is from then on.
+    if (OUT) {
+      const int id = threadIdx.x - 32 * kScanWarp;
+      for (int c = 0; c < n; ++c) {
+        const int uv = c * kUnits + kK + 1;
+        const bool there = full_wait(uv);
+        if (!group_all(2, 64, there)) break;
+        uint8_t* v = smem + (tile(uv) - sb);
+        uint32_t over = 0;                               // bits 15 and 31: an exponent of ones, + 1
+#pragma unroll 8
+        for (uint32_t at = id * 16; at < L::kTile; at += 64 * 16) {
+          const uint4 x = *reinterpret_cast<const uint4*>(v + at);
+          over |= ((x.x & 0x7f807f80u) + 0x00800080u) | ((x.y & 0x7f807f80u) + 0x00800080u) |
+                  ((x.z & 0x7f807f80u) + 0x00800080u) | ((x.w & 0x7f807f80u) + 0x00800080u);
+        }
+        const bool bad = !group_all(2, 64, (over & 0x80008000u) == 0u);
+        if (bad && (c >= n_state || mbar_wait(b_pd + 8 * (c & 1), (uint32_t)(c >> 1) & 1u, s_abort))) {
+          for (int col = id; col < DH; col += 64) {
+            uint8_t* half = v + (col / 64) * L::kHalf;
+            int first = C;
+            for (int j = C - 1; j >= 0; --j) {
+              uint16_t* e = reinterpret_cast<uint16_t*>(half + j * 128 + ((((col & 63) / 8) ^ (j & 7)) * 16)) + (col & 7);
+              if ((*e & 0x7f80u) == 0x7f80u) {
+                *e = 0;
+                first = j;
+              }
+            }
+            s_first[(c & 1) * DH + col] = (uint8_t)first;
+          }
+          asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+        }
+        if (id == 0) s_bad[c & 1] = bad ? 1 : 0;
+        mbar_arrive(b_vs + 8 * (c & 1));
+      }
     }
   } else {
     // ------------------------------------------------------------ state
@@ -676,7 +737,9 @@ recurrent_kernel(const RecurrentParams p) {
     S[i] = p.init != nullptr && RATP_IN(at, 4, n_s) ? __ldcs(reinterpret_cast<const float4*>(p.init + at))
                                                     : make_float4(0.f, 0.f, 0.f, 0.f);
   }
-  const Decay a = decay_pair(p.log_decay[h], 1.0);
+  const float ld = p.log_decay[h];
+  if (!(ld <= 0.f) && threadIdx.x == 0) raise_error(RATP_ERR_ARG);
+  const Decay a = decay_pair(ld, 1.0);
   for (int t = 0; t < p.T; ++t) {
     const long long row = (((long long)b * p.T + t) * p.H + h) * DH;
     const bool in = RATP_IN(row, DH, n_tok);

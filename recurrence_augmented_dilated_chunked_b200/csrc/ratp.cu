@@ -522,13 +522,25 @@ int launch_norm_rope(const norm_rope::Params& p, int Dh, cudaStream_t st) {
   return launch_status();
 }
 
-// a view of `heads` head rows: pointer, strides that keep rows 16-byte aligned
-int check_view(const ratp_view* v, int heads, int esize) {
+// a view of `heads` head rows: pointer, strides that keep rows 16-byte aligned;
+// of an output, also that no two of its rows overlap (each dimension's stride
+// passes all that the dimensions of smaller strides span)
+int check_view(const ratp_view* v, int heads, int esize, int B, int T, int Dh, bool output) {
   if (v == nullptr || v->data == nullptr || v->heads != heads) return RATP_ERR_ARG;
   if (v->stride_b < 0 || v->stride_t < 0 || v->stride_h < 0) return RATP_ERR_ARG;
   if (!aligned16(v->data)) return RATP_ERR_ALIGN;
   const long long q = 16 / esize;
   if (v->stride_b % q || v->stride_t % q || v->stride_h % q) return RATP_ERR_ALIGN;
+  if (output) {
+    std::pair<int64_t, int64_t> dim[3] = {{v->stride_b, B}, {v->stride_t, T}, {v->stride_h, heads}};
+    std::sort(dim, dim + 3);
+    int64_t span = Dh;
+    for (const auto& d : dim) {
+      if (d.second <= 1) continue;
+      if (d.first < span) return RATP_ERR_ARG;
+      span += d.first * (d.second - 1);
+    }
+  }
   return RATP_OK;
 }
 
@@ -1106,10 +1118,16 @@ int ratp_linear_attn_prefill(const void* q, const void* k, const void* v, const 
   LinearPlan pl;
   int rc = linear_plan(B, T, H, Dh, &pl);
   if (rc) return rc;
+  cudaStream_t st = static_cast<cudaStream_t>(stream);
+  if (T == 0 && (long long)B * H > 0 && final_state != nullptr && final_state != initial_state) {
+    const size_t n = (size_t)B * H * Dh * Dh * 4;        // no token: the state as it was
+    const cudaError_t e = initial_state != nullptr ? cudaMemcpyAsync(final_state, initial_state, n, cudaMemcpyDeviceToDevice, st)
+                                                   : cudaMemsetAsync(final_state, 0, n, st);
+    return e == cudaSuccess ? RATP_OK : RATP_ERR_CUDA;
+  }
   if ((long long)B * T * H == 0) return RATP_OK;
   rc = check_linear(q, k, v, log_decay, initial_state, final_state, o, scale, dtype);
   if (rc) return rc;
-  cudaStream_t st = static_cast<cudaStream_t>(stream);
   if (T <= linear_attn::kRecurrentTokens)
     return launch_linear_recurrent(q, k, v, log_decay, initial_state, final_state, o, B, T, H, Dh, scale, st);
   const size_t need = linear_ws_bytes(pl, B, H, Dh);
@@ -1175,10 +1193,9 @@ int ratp_qk_norm_rope(const ratp_view* q, const ratp_view* k, const ratp_view* q
       p.tensor[i].blk = 0;
       continue;
     }
-    for (const ratp_view* v : {in[i], out[i]}) {
-      const int rc = check_view(v, in[i]->heads, esize);
-      if (rc) return rc;
-    }
+    int rc = check_view(in[i], in[i]->heads, esize, B, T, Dh, false);
+    if (rc == RATP_OK) rc = check_view(out[i], in[i]->heads, esize, B, T, Dh, true);
+    if (rc) return rc;
     if (w[i] != nullptr && !aligned16(w[i])) return RATP_ERR_ALIGN;
     fill_norm_rope(&p.tensor[i], in[i], out[i], w[i], tokens);
     const long long n = tokens * p.tensor[i].n_blk;

@@ -195,6 +195,59 @@ def test_constant_groups_and_signed_zero_are_held_exactly():
     assert np.array_equal(cache.dil_rows("v").cpu().double().numpy(), held(to64(hv)[:, :, 0]))
 
 
+@pytest.mark.parametrize("bad", [float("nan"), float("inf"), -float("inf"), None])
+def test_a_group_that_is_not_finite_stands_for_nan(bad):
+    """None: finite values further apart than fp32 holds.  The rest of the cache,
+    and the heads and channels that do not read the group, are what they are
+    without it."""
+    B, H, Dh, T = 2, 2, 128, 70
+    g = torch.Generator().manual_seed(5)
+    hk, hv, q, xk, xv, gate = (torch.randn(B, n, H, Dh, generator=g).to(torch.bfloat16).to(DEV) for n in (T, T, 1, 1, 1, 1))
+    args = [x[:, 0].contiguous() for x in (q, xk, xv, gate.sigmoid())]
+
+    def run(k, v):
+        cache = ratp.KVCache(B, H, Dh, T + 1, 2, kv_bits=4)
+        cache.pack(k, v)
+        rows = [cache.dil_rows(w).clone() for w in "kv"]
+        return rows, cache.decode_step(*args, torch.zeros(2, B, H, Dh, device=DEV))
+
+    rows0, o0 = run(hk, hv)
+    for which in (0, 1):
+        x = [hk.clone(), hv.clone()]
+        x[which][1, 41, 0, 70] = 3.0e38 if bad is None else bad          # slot 20 of head 0, channels 64 .. 95
+        if bad is None:
+            x[which][1, 41, 0, 71] = -3.0e38
+        rows, o = run(*x)
+        hit = [torch.zeros_like(r, dtype=torch.bool) for r in rows]
+        hit[which][1, 20, 64:96] = True
+        for r, r0, m in zip(rows, rows0, hit):
+            assert torch.equal(r[~m], r0[~m])
+        assert bool(torch.isnan(rows[which][hit[which]]).all())
+        m = torch.zeros_like(o, dtype=torch.bool)
+        if which == 0:
+            m[1, 0] = True                          # a key's score: the whole head
+        else:
+            m[1, 0, 64:96] = True                   # a value: its channels
+        assert torch.equal(o[~m], o0[~m])
+        assert bool(torch.isnan(o[m]).all())
+    ratp.last_error()
+
+
+def test_tensors_of_another_shape_are_refused():
+    cache = ratp.KVCache(2, 2, 64, 16, 2, kv_bits=4)
+    x = torch.zeros(2, 2, 64, dtype=torch.bfloat16, device=DEV)
+    state = torch.zeros(2, 2, 2, 64, device=DEV)
+    prompt = torch.zeros(2, 8, 2, 64, dtype=torch.bfloat16, device=DEV)
+    short = x[:1].contiguous()
+    for call in (lambda: cache.decode_step(short, x, x, x, state), lambda: cache.decode_step(x, x, x, short, state),
+                 lambda: cache.decode_step(x, x, x, x, state[:1].contiguous()),
+                 lambda: cache.decode_step(x, x, x, x, state, out=short),
+                 lambda: ratp.decode_step_layers([(cache, x, x, short, x, state, x.clone())]),
+                 lambda: cache.pack(prompt[:1].contiguous(), prompt), lambda: cache.pack(prompt, prompt, T=9)):
+        with pytest.raises(ValueError):
+            call()
+
+
 def test_unequal_lengths_and_repacking():
     """Sequences of a batch at their own lengths, and a cache packed again."""
     B, H, Dh, T, D = 3, 2, 128, 64, 4

@@ -243,8 +243,70 @@ def test_step_of_a_full_batch():
     check(o[:, None], st, definition(q, k, v, ld, s0, Dh ** -0.5), 1, Dh, "step")
 
 
+@pytest.mark.parametrize("bad", [float("nan"), float("inf"), -float("inf")])
+@pytest.mark.parametrize("B,T,H,Dh,at,seen", [
+    (1, 128 * 9 + 30, 2, 128, 128 * 4 + 77, True),      # inside a segment's chunk
+    (1, 128 * 9 + 30, 2, 64, 128 * 9 + 20, True),       # in the last, ragged chunk
+    (2, 200, 1, 128, 127, True),
+    (2, 200, 1, 128, 199, False),                       # the last token, its state not asked for
+    (1, 11, 1, 64, 5, True),                            # token by token
+])
+def test_values_that_are_not_finite_leave_the_tokens_before_alone(B, T, H, Dh, at, seen, bad):
+    """One channel of v (then of k) at one token, as right padding may hold.
+    What it does not reach is bit for bit what it is without it: the products
+    with it were with zeros."""
+    q, k, v, ld, s0 = (x.to(DEV) for x in make(B, T, H, Dh, seed=12, decays=[-0.01, -0.5][:H]))
+    fin0 = torch.zeros(B, H, Dh, Dh, device=DEV)
+    o0 = ratp.linear_attn_prefill(q, k, v, ld, s0, fin0)
+    b, h, c = B - 1, H - 1, 37
+    for which in "vk":
+        x = {"v": v, "k": k}[which].clone()
+        x[b, at, h, c] = bad
+        fin = torch.zeros(B, H, Dh, Dh, device=DEV) if seen else None
+        o = ratp.linear_attn_prefill(q, x if which == "k" else k, x if which == "v" else v, ld, s0, fin)
+        hit = torch.zeros_like(o, dtype=torch.bool)
+        hit[b, at:, h, c if which == "v" else slice(None)] = True
+        assert bits_equal(o[~hit], o0[~hit]), which
+        assert not bool(torch.isfinite(o[hit].float()).any()), which
+        if seen:
+            hit = torch.zeros_like(fin, dtype=torch.bool)
+            if which == "v":
+                hit[b, h, :, c] = True
+            else:
+                hit[b, h, c, :] = True
+            assert bits_equal(fin[~hit], fin0[~hit]), which
+            assert not bool(torch.isfinite(fin[hit]).any()), which
+    ratp.last_error()
+
+
+@pytest.mark.parametrize("decay", [0.25, float("nan"), float("inf")])
+@pytest.mark.parametrize("T", [1, 300])
+def test_a_decay_that_grows_is_reported(T, decay):
+    q, k, v, ld, _ = (x.to(DEV) for x in make(1, T, 2, 64, seed=2, decays=[-0.1, decay], init=True))
+    ratp.linear_attn_prefill(q, k, v, ld)
+    with pytest.raises(ratp.RatpError):
+        ratp.last_error()
+    ratp.last_error()                               # reported once
+    if T == 1:
+        ratp.linear_attn_step(q[:, 0], k[:, 0], v[:, 0], ld, torch.zeros(1, 2, 64, 64, device=DEV))
+        with pytest.raises(ratp.RatpError):
+            ratp.last_error()
+
+
+def test_no_token_hands_the_state_on():
+    q, _, _, ld, s0 = (x.to(DEV) for x in make(2, 20, 2, 64, seed=1))
+    none = q[:, :0].contiguous()
+    fin = torch.full_like(s0, 3.0)
+    ratp.linear_attn_prefill(none, none, none, ld, s0, fin)
+    assert bits_equal(fin, s0)
+    ratp.linear_attn_prefill(none, none, none, ld, None, fin)
+    assert not bool(fin.any())
+
+
 def test_refusals():
     q, k, v, ld, s0 = (x.to(DEV) for x in make(1, 20, 2, 64, seed=1))
+    flat = torch.zeros(4 * q.numel(), dtype=torch.bfloat16, device=DEV)      # an out that begins inside v
+    both = [flat[i * q.numel() - (64 if i == 3 else 0):][:q.numel()].view(q.shape) for i in range(4)]
     bad = [
         lambda: ratp.linear_attn_prefill(q.float(), k, v, ld),
         lambda: ratp.linear_attn_prefill(q, k[:, :10], v, ld),
@@ -257,6 +319,10 @@ def test_refusals():
         lambda: ratp.linear_attn_prefill(q.cpu(), k.cpu(), v.cpu(), ld.cpu()),
         lambda: ratp.linear_attn_step(q[:, 0].contiguous(), k[:, 0].contiguous(), v[:, 0].contiguous(), ld, None),
         lambda: ratp.linear_attn_step(q, k, v, ld, s0),
+        lambda: ratp.linear_attn_prefill(q, k, v, ld, out=v),
+        lambda: ratp.linear_attn_prefill(*both[:3], ld, out=both[3]),
+        lambda: ratp.linear_attn_prefill(q, k, v, ld, workspace=torch.empty(1 << 20, dtype=torch.uint8)),
+        lambda: ratp.linear_attn_prefill(q, k, v, ld, workspace=torch.empty(1 << 20, device=DEV)),
     ]
     for call in bad:
         with pytest.raises(ValueError):

@@ -55,6 +55,9 @@ def test_norm_rope_refusals(lib):
     assert norm(lib, w=4100) == ALIGN
     assert norm(lib, f=4100) == ALIGN
     assert norm(lib, pos=4098) == ALIGN
+    # outputs whose own rows overlap: broadcast tokens, heads closer than a row
+    assert norm(lib, qo=view(st=0)) == ARG and norm(lib, ko=view(sh=64)) == ARG and norm(lib, ko=view(st=128)) == ARG
+    assert norm(lib, B=2, ko=view(sb=1024)) == ARG        # 4 tokens of 512
     # nothing to do, nothing launched
     assert norm(lib, B=0) == 0 and norm(lib, T=0) == 0
     none = view(data=0, heads=0)
