@@ -28,7 +28,7 @@
 // segment's own state (from zero), combine_kernel turns those into the state
 // before each segment, and chunk_kernel<DH, true> runs all segments at once.
 //
-// Roles of chunk_kernel (512 threads, one CTA per SM):
+// Roles of chunk_kernel (448 threads, one CTA per SM):
 //   warps 0-3   P: read Q K^T from TMEM, mask, decay, write bf16 P to TMEM over
 //               it; then o = scale a^{i+1} O1 + O2 out of TMEM to memory;
 //   warps 4-11  state, half of its columns to each four warps: scale K in place
@@ -40,9 +40,14 @@
 //               O1 = Q S, O2 = P V, SL = K'^T V (M = Dh).  Q K^T of the next
 //               chunk goes between the first and the other parts of SL, so that
 //               P of the next chunk is worked out while this one's state is.
-//   warps 14, 15  keep values that are not finite out of the outputs before them.
 //   Without an output (<DH, false>) only SL is computed, in two buffers, and
 //   warps 0-3 share the scaling of K.
+// P V multiplies the values of the tokens after i by zeros, so a value that is not
+// finite would reach the outputs of its chunk before it.  It also stays in the
+// state, so one look at the last chunk's o tells whether a CTA met any; if so, it
+// does its chunks over in a pass that takes such values out of V once the state's
+// products have read them (4 x 8192 x 32 x 128: 240 us; with V scanned in every
+// pass, by two more warps, 306 us).
 // Bound: 4 tiles of memory traffic per chunk and (b, h) against six products.
 #pragma once
 #include "sm100.cuh"
@@ -51,11 +56,10 @@ namespace ratp {
 namespace linear_attn {
 
 constexpr int C = 128;                 // tokens per chunk
-constexpr int kThreads = 512;
+constexpr int kThreads = 448;
 constexpr int kStateWarps = 8;         // warps 4 .. 11
 constexpr int kProducerWarp = 12;
 constexpr int kMmaWarp = 13;
-constexpr int kScanWarp = 14;          // and 15
 constexpr int kSlots = 5;
 constexpr int kPart = 32;               // tokens whose scaled K is handed to the MMA at a time
 constexpr int kParts = C / kPart;
@@ -91,11 +95,11 @@ struct Layout {
   static constexpr uint32_t kOffPow = kOffS + (DH / 64) * kSHalf;    // a^0 .. a^128
   static constexpr uint32_t kOffDecay = kOffPow + (C + 2) * 4;       // of a whole chunk, of the sequence's last
   static constexpr uint32_t kOffBar = kOffDecay + 2 * sizeof(Decay);
-  static constexpr int kBars = 2 * kSlots + 17;
-  static constexpr uint32_t kOffCtl = kOffBar + kBars * 8;           // TMEM address, abort flag, bad[2]
-  static constexpr uint32_t kOffFirst = kOffCtl + 16;                // first[2][DH], bytes
+  static constexpr int kBars = 2 * kSlots + 15;                      // of a pass; there are two
+  static constexpr uint32_t kOffCtl = kOffBar + 2 * kBars * 8;       // TMEM address, abort flag
+  static constexpr uint32_t kOffFirst = kOffCtl + 16;                // first[DH], bytes
   // one CTA per SM whatever DH, since each takes all of TMEM
-  static constexpr uint32_t kUsed = kOffFirst + 2 * DH + 1024;
+  static constexpr uint32_t kUsed = kOffFirst + DH + 1024;
   static constexpr uint32_t kBytes = kUsed > 120 * 1024 ? kUsed : 120 * 1024;
 };
 static_assert(Layout<128>::kBytes <= 232448, "shared memory of one CTA");
@@ -143,20 +147,18 @@ __device__ __forceinline__ bool group_all(int id, int count, bool ok) {
   return r != 0;
 }
 
-template <int DH, bool OUT>
-__global__ void __launch_bounds__(kThreads, 1)
-chunk_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
-             const __grid_constant__ CUtensorMap tm_v, const __grid_constant__ CUtensorMap tm_o,
-             const __grid_constant__ Params p) {
+// One pass over a CTA's chunks.  REPAIR: the pass that does them over, with the
+// values that are not finite taken out of P V.  Returns whether that is needed.
+template <int DH, bool OUT, bool REPAIR>
+__device__ __forceinline__ bool chunk_pass(const CUtensorMap& tm_q, const CUtensorMap& tm_k, const CUtensorMap& tm_v,
+                                           const CUtensorMap& tm_o, const Params& p, uint8_t* smem, uint32_t tmem) {
   using namespace sm100;
   using L = Layout<DH>;
   constexpr int NH = DH / 64;                            // 64-channel halves
   constexpr int kUnits = OUT ? 3 : 2;                    // tiles per chunk: (Q,) K, V
   constexpr int kK = OUT ? 1 : 0;                        // K's place among them
-  extern __shared__ uint8_t smem_raw[];
-  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   const uint32_t sb = smem_u32(smem);
-  const uint32_t bar0 = sb + L::kOffBar;
+  const uint32_t bar0 = sb + L::kOffBar + (REPAIR ? L::kBars * 8u : 0u);
   const uint32_t b_full = bar0, b_empty = bar0 + 8 * kSlots;
   const uint32_t b_qk = bar0 + 8 * (2 * kSlots), b_p = b_qk + 8, b_o = b_qk + 16, b_ofree = b_qk + 24;
   // part g = kParts c + part of this CTA's tokens uses buffer g & 1, and these
@@ -168,13 +170,10 @@ chunk_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ C
   // barriers [c & 1], phase c / 2
   const uint32_t b_pd = b_qk + 80, b_sf = b_qk + 96;
   const uint32_t b_qs = b_qk + 112;                      // Q S done
-  const uint32_t b_vs = b_qk + 120;                      // [2]: V of chunk c is finite, barrier [c & 1]
   float* s_pow = reinterpret_cast<float*>(smem + L::kOffPow);
   Decay* s_decay = reinterpret_cast<Decay*>(smem + L::kOffDecay);
-  uint32_t* s_tmem = reinterpret_cast<uint32_t*>(smem + L::kOffCtl);
   volatile int* s_abort = reinterpret_cast<volatile int*>(smem + L::kOffCtl + 4);
-  int* s_bad = reinterpret_cast<int*>(smem + L::kOffCtl + 8);        // [c & 1]: V of chunk c was not finite,
-  uint8_t* s_first = smem + L::kOffFirst;                            // column x from token s_first[c & 1][x] on
+  [[maybe_unused]] uint8_t* s_first = smem + L::kOffFirst;           // column x of V is not finite from token s_first[x] on
   const int warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;   // warp: known uniform
 
   // segment `seg` of (b, h)
@@ -191,7 +190,6 @@ chunk_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ C
   auto tokens = [&](int c) { return min(C, p.T - (c0 + c) * C); };
 
   if (threadIdx.x == 0) {
-    *s_abort = 0;
     for (int i = 0; i < kSlots; ++i) {
       mbar_init(b_full + 8 * i, 1);
       mbar_init(b_empty + 8 * i, 1);
@@ -206,25 +204,14 @@ chunk_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ C
       mbar_init(b_kv + 8 * i, 1);
       mbar_init(b_pd + 8 * i, 1);
       mbar_init(b_sf + 8 * i, 32 * kStateWarps);
-      mbar_init(b_vs + 8 * i, 64);
     }
     mbar_init(b_s, 32 * kStateWarps);
     mbar_init(b_final, 1);
     fence_barrier_init();
   }
-  if (warp == kMmaWarp) {
-    tmem_alloc(smem_u32(s_tmem), kTmemCols);
-    tmem_relinquish();
-  }
   const float ld = p.log_decay[h];
-  if (!(ld <= 0.f) && seg == 0 && threadIdx.x == 0) raise_error(RATP_ERR_ARG);
-  if (threadIdx.x <= C) s_pow[threadIdx.x] = decay_power(ld, (double)threadIdx.x);
-  else if (threadIdx.x <= C + 2)
-    s_decay[threadIdx.x - C - 1] = decay_pair(ld, threadIdx.x == C + 1 ? (double)C : (double)(p.T - (p.n_chunks - 1) * C));
-  tc_fence_before();
   __syncthreads();
-  tc_fence_after();
-  const uint32_t tmem = *s_tmem;
+  bool again = false;                                    // known to warp 0 and the state warps
   // tile u of this CTA (chunk u / kUnits; (Q,) K, V in turn) lies in slot u % kSlots
   auto full_wait = [&](int u) { return mbar_wait(b_full + 8 * (u % kSlots), (uint32_t)(u / kSlots) & 1u, s_abort); };
   auto tile = [&](int u) { return sb + (uint32_t)(u % kSlots) * L::kTile; };
@@ -387,16 +374,16 @@ chunk_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ C
         __syncwarp();
       }
       if (!ok) break;
-      if (c < n_state && elect_one()) umma_commit(b_pd + 8 * (c & 1));
-      __syncwarp();
+      if (REPAIR) {                                      // V is repaired after these products
+        if (c < n_state && elect_one()) umma_commit(b_pd + 8 * (c & 1));
+        __syncwarp();
+      }
       // P is there and O holds the scaled Q S.  These products and the next
       // chunk's Q K^T run while the state warps bring S forward.
-      if (OUT && !warp_all(mbar_wait(b_p, par, s_abort) && mbar_wait(b_vs + 8 * (c & 1), (uint32_t)(c >> 1) & 1u, s_abort))) {
-        ok = false;
-        break;
-      }
+      if (OUT && !warp_all(mbar_wait(b_p, par, s_abort))) { ok = false; break; }
       tc_fence_after();
       if (elect_one()) {
+        if (!REPAIR && c < n_state) umma_commit(b_pd + 8 * (c & 1));   // with the rest: 240 us, ahead as above: 245
         if (OUT) {
 #pragma unroll
           for (int k = 0; k < C / 16; ++k)
@@ -486,22 +473,39 @@ chunk_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ C
         }
         tmem_wait_st();
         tc_fence_before();
+        if (REPAIR) {
+          const int uv = c * kUnits + kK + 1;
+          if (!warp_all(full_wait(uv) && (c >= n_state || mbar_wait(b_pd + 8 * (c & 1), (uint32_t)(c >> 1) & 1u, s_abort))))
+            return false;
+          if (i < DH) {                                  // column i of V
+            uint8_t* half = smem + (tile(uv) - sb) + (i / 64) * L::kHalf;
+            int first = C;
+            for (int j = C - 1; j >= 0; --j) {
+              uint16_t* e = reinterpret_cast<uint16_t*>(half + j * 128 + ((((i & 63) / 8) ^ (j & 7)) * 16)) + (i & 7);
+              if ((*e & 0x7f80u) == 0x7f80u) {
+                *e = 0;
+                first = j;
+              }
+            }
+            s_first[i] = (uint8_t)first;                 // the last chunk's are read
+          }
+          asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+        }
         mbar_arrive(b_p);
         return true;
       };
       // o through a staging tile, so that a copy writes whole rows
       auto work_o = [&](int c) {
         tc_fence_after();
-        const bool bad = s_bad[c & 1] != 0;
 #pragma unroll 2
         for (int q = 0; q < DH / 32; ++q) {
           uint32_t r[32];
           tmem_ld32(tl + kColO + 32 * q, r);
           tmem_wait_ld();
-          if (bad) {                                     // the columns of V that were not finite, from their token on
+          if (REPAIR) {
 #pragma unroll
             for (int x = 0; x < 32; ++x)
-              if (s_first[(c & 1) * DH + 32 * q + x] <= i) r[x] = 0x7fffffffu;
+              if (s_first[32 * q + x] <= i) r[x] = 0x7fffffffu;
           }
           if (q + 1 == DH / 32) {
             tc_fence_before();
@@ -527,8 +531,7 @@ chunk_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ C
         }
       };
       for (int c = 0; c < n; ++c) {
-        const bool there = work_p(c) && warp_all(mbar_wait(b_o, (uint32_t)c & 1u, s_abort) &&
-                                                 mbar_wait(b_vs + 8 * (c & 1), (uint32_t)(c >> 1) & 1u, s_abort));
+        const bool there = work_p(c) && warp_all(mbar_wait(b_o, (uint32_t)c & 1u, s_abort));
         // the copy of the chunk before has read the staging tile; the four warps
         // go on, or give up, together
         if (threadIdx.x == 0) asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory");
@@ -536,50 +539,17 @@ chunk_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ C
         work_o(c);
       }
       if (threadIdx.x == 0) asm volatile("cp.async.bulk.wait_group 0;" ::: "memory");
+      if (!REPAIR && warp == 0) {                        // o of the last chunk's first token: finite?
+        uint32_t over = 0u;                              // bits 15 and 31: an exponent of ones, + 1
+#pragma unroll
+        for (int hf = 0; hf < NH; ++hf)
+          over |= (reinterpret_cast<const uint32_t*>(smem + L::kOffO + hf * L::kHalf)[lane] & 0x7f807f80u) + 0x00800080u;
+        again = !group_all(2, 32 + 32 * kStateWarps, (over & 0x80008000u) == 0u || *s_abort != 0);
+      }
     } else {
       // parts 0 and 2; the state warps' second half has 1 and 3
       for (int c = 0; c < n; ++c)
         if (!warp_all(full_wait(c * kUnits + kK)) || !scale_k(c, 0, 2)) break;
-    }
-  } else if (warp >= kScanWarp) {
-    // ------------------------------------------------------------ scan of V
-    // P V multiplies the values of the tokens after i by zeros, so that one which
-    // is not finite would reach the outputs before it.  Where a tile has any, they
-    // are made zeros once the state's products have read them, and the outputs
-    // from their token on are made NaN, as the state is from then on.
-    if (OUT) {
-      const int id = threadIdx.x - 32 * kScanWarp;
-      for (int c = 0; c < n; ++c) {
-        const int uv = c * kUnits + kK + 1;
-        const bool there = full_wait(uv);
-        if (!group_all(2, 64, there)) break;
-        uint8_t* v = smem + (tile(uv) - sb);
-        uint32_t over = 0;                               // bits 15 and 31: an exponent of ones, + 1
-#pragma unroll 8
-        for (uint32_t at = id * 16; at < L::kTile; at += 64 * 16) {
-          const uint4 x = *reinterpret_cast<const uint4*>(v + at);
-          over |= ((x.x & 0x7f807f80u) + 0x00800080u) | ((x.y & 0x7f807f80u) + 0x00800080u) |
-                  ((x.z & 0x7f807f80u) + 0x00800080u) | ((x.w & 0x7f807f80u) + 0x00800080u);
-        }
-        const bool bad = !group_all(2, 64, (over & 0x80008000u) == 0u);
-        if (bad && (c >= n_state || mbar_wait(b_pd + 8 * (c & 1), (uint32_t)(c >> 1) & 1u, s_abort))) {
-          for (int col = id; col < DH; col += 64) {
-            uint8_t* half = v + (col / 64) * L::kHalf;
-            int first = C;
-            for (int j = C - 1; j >= 0; --j) {
-              uint16_t* e = reinterpret_cast<uint16_t*>(half + j * 128 + ((((col & 63) / 8) ^ (j & 7)) * 16)) + (col & 7);
-              if ((*e & 0x7f80u) == 0x7f80u) {
-                *e = 0;
-                first = j;
-              }
-            }
-            s_first[(c & 1) * DH + col] = (uint8_t)first;
-          }
-          asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
-        }
-        if (id == 0) s_bad[c & 1] = bad ? 1 : 0;
-        mbar_arrive(b_vs + 8 * (c & 1));
-      }
     }
   } else {
     // ------------------------------------------------------------ state
@@ -656,9 +626,12 @@ chunk_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ C
         }
       }
     }
+    // a state that will be computed again is not written: it may lie where the
+    // initial one is read from
+    if (OUT && !REPAIR) again = !group_all(2, 32 + 32 * kStateWarps, true);
     float* dst = OUT ? (want_end ? p.fin + (size_t)pair * DH * DH : nullptr)
                      : p.ws + ((size_t)pair * p.n_seg + seg) * DH * DH;
-    if (ok && mine && dst != nullptr) {
+    if (ok && !again && mine && dst != nullptr) {
 #pragma unroll
       for (int x = 0; x < NC; x += 4)
         *reinterpret_cast<float4*>(dst + at + x) = make_float4(S[x], S[x + 1], S[x + 2], S[x + 3]);
@@ -666,11 +639,52 @@ chunk_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ C
   }
 
   tc_fence_before();
-  __syncthreads();
+  const bool any = __syncthreads_or(again);
+  tc_fence_after();
+  return any;
+}
+
+template <int DH>
+__device__ __noinline__ void repair_pass(const CUtensorMap& tm_q, const CUtensorMap& tm_k, const CUtensorMap& tm_v,
+                                         const CUtensorMap& tm_o, const Params& p, uint8_t* smem, uint32_t tmem) {
+  chunk_pass<DH, true, true>(tm_q, tm_k, tm_v, tm_o, p, smem, tmem);
+}
+
+template <int DH, bool OUT>
+__global__ void __launch_bounds__(kThreads, 1)
+chunk_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
+             const __grid_constant__ CUtensorMap tm_v, const __grid_constant__ CUtensorMap tm_o,
+             const __grid_constant__ Params p) {
+  using namespace sm100;
+  using L = Layout<DH>;
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  float* s_pow = reinterpret_cast<float*>(smem + L::kOffPow);
+  Decay* s_decay = reinterpret_cast<Decay*>(smem + L::kOffDecay);
+  uint32_t* s_tmem = reinterpret_cast<uint32_t*>(smem + L::kOffCtl);
+  const int warp = threadIdx.x >> 5;
+  const int per = OUT ? p.n_seg : p.n_seg - 1, pair = blockIdx.x / per;
   if (warp == kMmaWarp) {
-    tc_fence_after();
-    tmem_dealloc(tmem, kTmemCols);
+    tmem_alloc(smem_u32(s_tmem), kTmemCols);
+    tmem_relinquish();
   }
+  const float ld = p.log_decay[pair % p.H];
+  if (threadIdx.x == 0) {
+    *reinterpret_cast<volatile int*>(smem + L::kOffCtl + 4) = 0;
+    if (!(ld <= 0.f)) raise_error(RATP_ERR_ARG);
+  }
+  if (threadIdx.x <= C) s_pow[threadIdx.x] = decay_power(ld, (double)threadIdx.x);
+  else if (threadIdx.x <= C + 2)
+    s_decay[threadIdx.x - C - 1] = decay_pair(ld, threadIdx.x == C + 1 ? (double)C : (double)(p.T - (p.n_chunks - 1) * C));
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = *s_tmem;
+  const bool again = chunk_pass<DH, OUT, false>(tm_q, tm_k, tm_v, tm_o, p, smem, tmem);
+  if constexpr (OUT) {
+    if (again) repair_pass<DH>(tm_q, tm_k, tm_v, tm_o, p, smem, tmem);
+  }
+  if (warp == kMmaWarp) tmem_dealloc(tmem, kTmemCols);
 }
 
 // Segment states -> the state before each segment, in place: element e of
