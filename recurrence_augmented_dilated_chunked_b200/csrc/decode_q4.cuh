@@ -37,6 +37,11 @@
 //           minima are taken out in fp32 against those same parts.
 // Ring rows are bf16 already and go through the same accumulators with
 // weights p.
+// Measured (floors at 6.55 TB/s): 64 sequences x 16 heads of 512 slots and a
+// window of 128, 42.5 us of 23.5; 4 x 32 heads of 8192 slots, 46 us of 25.7.
+// About 8 us are the step's start and end (length, inputs, merge, closing
+// counters); the rest streams at 4.5 TB/s, held by the expansion of the codes as
+// much as by memory (with the products left out the second case took 37 us).
 #pragma once
 #include "common.cuh"
 #include "decode.cuh"
@@ -54,8 +59,8 @@ constexpr int kWarps = kThreads / 32;
 constexpr int kTile = 16;          // keys per MMA tile
 constexpr int kStep = 32;          // cached rows per warp step
 constexpr int kRingStep = 8;       // ring rows per warp step (their bytes fit the same stage)
-constexpr int kStages = 2;         // steps in flight per warp
-constexpr int kCtasPerSm = 8;
+constexpr int kStages = 2;         // steps in flight per warp (20 KB of blocks a CTA)
+constexpr int kCtasPerSm = 8;      // 16 warps of 128 registers
 constexpr int kGroup = 32;         // channels per scale
 // A ring key moves 512 bytes where a 4-bit key moves 160: it counts as three
 // when a (b, h)'s keys are split over CTAs.
@@ -193,6 +198,9 @@ __device__ __forceinline__ int head_at(const int* base, int H, int at) {
 // Heads take blocks as they need (base[h]): a dense head has D times a dilated
 // one's rows.  A thread has all its rows' loads in flight at once, and the
 // block's index arithmetic and a group's parameters are spread over 16 channels.
+// Bound by its reads and, close behind, by the arithmetic of the codes: 4 x 8192
+// tokens of 2 dense heads and 30 of D = 4 (210 MB) take 45.5 us, 4.6 TB/s (with 8
+// channels a thread 57.6 us).
 constexpr int kPackRows = 2;
 template <int DH>
 __global__ void __launch_bounds__(256)
@@ -257,7 +265,8 @@ pack_kernel(const __grid_constant__ PackParams pp) {
 
 // ---- read-back: the values that the held rows stand for, fp32 ------------------
 // A CTA reads one block of slots; a thread has quads of 4 channels, 256 apart, so
-// that every store of a warp is 512 contiguous bytes.
+// that every store of a warp is 512 contiguous bytes.  Bound by its writes (8 times
+// the codes): 311 000 rows of 128 channels take 31 us, 5.8 TB/s.
 struct ReadParams {
   const void* blocks;
   float* out;                      // [B][rows_per_b][Dh]
@@ -322,19 +331,10 @@ struct Lane {
   static constexpr int NV = DH / 64;           // V words per key and lane (an eighth)
 };
 
-// 16 bytes to shared memory; with there == false, zeros.
-__device__ __forceinline__ void cp_async16(uint32_t dst, const void* src, bool there) {
-  const int n = there ? 16 : 0;
-  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" :: "r"(dst), "l"(src), "r"(n) : "memory");
-}
-
-// A block into shared memory as one copy; completes on `bar`.  One thread.
-template <int DH>
-__device__ __forceinline__ void fetch_block(uint32_t stage, const Block<DH>* src, uint32_t bar) {
-  constexpr uint32_t kBytes = (uint32_t)sizeof(Block<DH>);
-  sm100::mbar_arrive_expect_tx(bar, kBytes);
+// Copy to shared memory, completing on `bar`.  One thread; 16-byte multiples.
+__device__ __forceinline__ void bulk_load(uint32_t dst, const void* src, uint32_t bytes, uint32_t bar) {
   asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];"
-               :: "r"(stage), "l"(src), "r"(kBytes), "r"(bar) : "memory");
+               :: "r"(dst), "l"(src), "r"(bytes), "r"(bar) : "memory");
 }
 
 template <int N>
@@ -480,37 +480,28 @@ __device__ __forceinline__ void attend_codes(Acc<DH>& a, const Block<DH>& st, co
 }
 
 // ---- ring rows: bf16, kRingStep of them in a stage ------------------------------
-// 16-byte chunk c of row r (quarter c / (DH / 32) of the channels) lies at
-// chunk place(c) of its row, which spreads the lanes' reads over the banks.
+// One copy a row, into rows 16 bytes apart from a multiple of the banks, which
+// leaves the lanes' reads two to a bank.
 template <int DH>
 struct RingStage {
-  uint4 k[kRingStep][DH / 8];
-  uint4 v[kRingStep][DH / 8];
+  uint4 k[kRingStep][DH / 8 + 1];
+  uint4 v[kRingStep][DH / 8 + 1];
 };
 
-template <int DH>
-__device__ __forceinline__ int ring_place(int c, int r) {
-  constexpr int Q = DH / 32;                   // chunks per quarter
-  return (c / Q + 4 * (c % Q)) ^ (((r & 1) << 2) | ((r >> 1) & 3));
-}
-
 // n <= kRingStep ring rows from ring row `first` on (wrapping at W) into a
-// stage; the rest zero.  Chunk i of a lane is row (32 i + lane) / (DH / 8).
+// stage, by the warp.
 template <int DH>
 __device__ __forceinline__ void fetch_ring(uint32_t stage, const __nv_bfloat16* kw, const __nv_bfloat16* vw, int first,
-                                           int W, int n, int lane) {
-  constexpr int NC = DH / 8, kRowsPer = 32 / NC;
-  const int r0 = lane / NC, c = lane % NC;
-#pragma unroll
-  for (int i = 0; i < kRingStep / kRowsPer; ++i) {
-    const int r = i * kRowsPer + r0;
-    int row = first + r;
-    row = row < W ? row : row - W;
-    if (r >= n) row = first;                   // any row of the ring: not read
-    const long long off = (long long)row * (DH * 2) + c * 16;
-    const uint32_t dst = stage + (uint32_t)(r * NC + ring_place<DH>(c, r)) * 16;
-    cp_async16(dst, reinterpret_cast<const char*>(kw) + off, r < n);
-    cp_async16(dst + (uint32_t)offsetof(RingStage<DH>, v), reinterpret_cast<const char*>(vw) + off, r < n);
+                                           int W, int n, int lane, uint32_t bar) {
+  constexpr uint32_t kRow = DH * 2;
+  static_assert(kRingStep == 8, "lanes 0..7 K, 8..15 V");
+  if (lane == 0) sm100::mbar_arrive_expect_tx(bar, 2u * kRow * (uint32_t)n);
+  __syncwarp();
+  const int r = lane & 7;
+  if (lane < 16 && r < n) {
+    const int row = first + r < W ? first + r : first + r - W;
+    const uint32_t dst = stage + (uint32_t)r * (kRow + 16) + (lane < 8 ? 0u : (uint32_t)offsetof(RingStage<DH>, v));
+    bulk_load(dst, (lane < 8 ? kw : vw) + (long long)row * DH, kRow, bar);
   }
 }
 
@@ -523,7 +514,7 @@ __device__ __forceinline__ void attend_ring(Acc<DH>& a, const RingStage<DH>& st,
   float d[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
   for (int w = 0; w < NW; ++w) {
-    const uint4 k = st.k[g][ring_place<DH>(t * NW + w, g)];
+    const uint4 k = st.k[g][t * NW + w];
     mma_bf16(d, k.x, 0u, k.y, 0u, qf[2 * w][0], qf[2 * w][1]);
     mma_bf16(d, k.z, 0u, k.w, 0u, qf[2 * w + 1][0], qf[2 * w + 1][1]);
   }
@@ -537,7 +528,7 @@ __device__ __forceinline__ void attend_ring(Acc<DH>& a, const RingStage<DH>& st,
   split_weights(pw, g < 4 ? 0.f : 1.f, bw, &got);
 #pragma unroll
   for (int w = 0; w < NV; ++w) {
-    const uint4 v0 = st.v[t][ring_place<DH>(g * NV + w, t)], v1 = st.v[4 + t][ring_place<DH>(g * NV + w, 4 + t)];
+    const uint4 v0 = st.v[t][g * NV + w], v1 = st.v[4 + t][g * NV + w];
     const uint32_t x[4] = {v0.x, v0.y, v0.z, v0.w}, y[4] = {v1.x, v1.y, v1.z, v1.w};
 #pragma unroll
     for (int i = 0; i < 4; ++i)
@@ -636,8 +627,7 @@ decode_kernel(const Params pp) {
     const int k0 = (int)min((long long)n_slots, u0) + warp * kStep;      // u0 is whole blocks
     Block<DH>* const stages = reinterpret_cast<Block<DH>*>(s_stages) + warp * kStages;
     const uint32_t stage0 = sm100::smem_u32(stages), bar0 = sm100::smem_u32(&s_bar[warp][0]);
-    // a warp's steps: rows k0 + i kRows .. of the cache, then its share of the
-    // ring; one commit group per step, empty past the end
+    // a warp's steps: rows k0 + i kRows .. of the cache, then its share of the ring
     constexpr int kRows = kWarps * kStep;
     const int r_begin = ring_at(u0), r_end = RATP_IN(bh * p.W * DH, (long long)p.W * DH, n_ring) ? ring_at(u1) : 0;
     const __nv_bfloat16* kw = p.Kw + bh * p.W * DH;
@@ -649,15 +639,17 @@ decode_kernel(const Params pp) {
     auto fetch_next = [&]() {
       const uint32_t stage = stage0 + fill * (uint32_t)sizeof(Block<DH>);
       if (at < s_end) {
-        if (lane == 0 && RATP_IN(block0 + at / kStep, 1, n_blocks)) fetch_block<DH>(stage, blocks + at / kStep, bar0 + 8 * fill);
+        if (lane == 0 && RATP_IN(block0 + at / kStep, 1, n_blocks)) {
+          sm100::mbar_arrive_expect_tx(bar0 + 8 * fill, (uint32_t)sizeof(Block<DH>));
+          bulk_load(stage, blocks + at / kStep, (uint32_t)sizeof(Block<DH>), bar0 + 8 * fill);
+        }
         at += kRows;
       } else if (ring < r_end) {
-        fetch_ring<DH>(stage, kw, vw, ring_row, p.W, min(kRingStep, r_end - ring), lane);
+        fetch_ring<DH>(stage, kw, vw, ring_row, p.W, min(kRingStep, r_end - ring), lane, bar0 + 8 * fill);
         ring += kWarps * kRingStep;
         ring_row += ring_hop;
         ring_row = ring_row < p.W ? ring_row : ring_row - p.W;
       }
-      asm volatile("cp.async.commit_group;" ::: "memory");
       fill = fill + 1 == kStages ? 0 : fill + 1;
     };
 #pragma unroll
@@ -718,37 +710,42 @@ decode_kernel(const Params pp) {
 
     int use = 0;
     uint32_t phase = 0;                        // of the barrier of stage `use`
-    for (int k = k0; k < s_end; k += kRows) {
-      fetch_next();
-      if (!sm100::warp_all(sm100::mbar_wait(bar0 + 8 * use, phase, &s_abort))) {
-        // every copy under way lands before the CTA ends: this one, and the ones
-        // fetched ahead of it
-        for (int i = 0, kk = k; i < kStages && kk < s_end; ++i, kk += kRows) {
-          sm100::mbar_drain(bar0 + 8 * use, phase);
-          use = use + 1 == kStages ? 0 : use + 1;
-          phase ^= use == 0 ? 1u : 0u;
-        }
-        at = s_end;
-        break;
-      }
-      if (s_end - k < kStep) {                 // rows past the last slot hold anything: 0 times their step must be 0
-        uint32_t* par = &stages[use].vp[0][0];
-        for (int i = (s_end - k) * (DH / kGroup) + lane; i < kStep * (DH / kGroup); i += 32) par[i] = 0u;
-        __syncwarp();
-      }
-      attend_codes<DH>(a, stages[use], qf, qsum, p.scale_log2, s_end - k, g, tq);
+    auto landed = [&]() { return sm100::warp_all(sm100::mbar_wait(bar0 + 8 * use, phase, &s_abort)); };
+    auto next = [&]() {
       __syncwarp();
       use = use + 1 == kStages ? 0 : use + 1;
       phase ^= use == 0 ? 1u : 0u;
-    }
-    for (int r = r_begin + warp * kRingStep; r < r_end; r += kWarps * kRingStep) {
+    };
+    int k = k0, r = r_begin + warp * kRingStep;
+    for (; k < s_end; k += kRows) {
       fetch_next();
-      asm volatile("cp.async.wait_group %0;" :: "n"(kStages - 1) : "memory");
-      __syncwarp();
-      attend_ring<DH>(a, reinterpret_cast<const RingStage<DH>&>(stages[use]), qf, p.scale_log2, min(kRingStep, r_end - r),
-                      g, tq);
-      __syncwarp();
-      use = use + 1 == kStages ? 0 : use + 1;
+      if (!landed()) break;
+      if (s_end - k < kStep) {                 // rows past the last slot hold anything: 0 times their step must be 0
+        uint32_t* par = &stages[use].vp[0][0];
+        for (int i = (s_end - k) * (DH / kGroup) + lane; i < kStep * (DH / kGroup); i += 32) par[i] = 0u;
+        asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+        __syncwarp();
+      }
+      attend_codes<DH>(a, stages[use], qf, qsum, p.scale_log2, s_end - k, g, tq);
+      next();
+    }
+    for (; k >= s_end && r < r_end; r += kWarps * kRingStep) {
+      fetch_next();
+      if (!landed()) break;
+      RingStage<DH>& st = reinterpret_cast<RingStage<DH>&>(stages[use]);
+      if (r_end - r < kRingStep) {             // likewise the values past the last row
+        uint4* v = &st.v[0][0];
+        for (int i = (r_end - r) * (DH / 8 + 1) + lane; i < kRingStep * (DH / 8 + 1); i += 32) v[i] = make_uint4(0u, 0u, 0u, 0u);
+        __syncwarp();
+      }
+      attend_ring<DH>(a, st, qf, p.scale_log2, min(kRingStep, r_end - r), g, tq);
+      next();
+    }
+    // given up: every copy under way lands before the CTA ends
+    for (int i = 0; i < kStages && (k < s_end || r < r_end); ++i) {
+      sm100::mbar_drain(bar0 + 8 * use, phase);
+      next();
+      if (k < s_end) k += kRows; else r += kWarps * kRingStep;
     }
 
     // ---- this warp's entry ----

@@ -502,11 +502,10 @@ void fill_norm_rope(norm_rope::Tensor* a, const ratp_view* x, const ratp_view* y
   a->ys_b = y->stride_b; a->ys_t = y->stride_t; a->ys_h = y->stride_h;
   a->H = x->heads;
   // A token's heads stay in one group of lanes, which computes its sines once,
-  // unless the tokens alone cannot fill the GPU (kGroups groups of 16 lanes
-  // are resident); then they are split into blocks of whole unrolled steps.
-  const long long kGroups = (long long)sm_count() * 128;
+  // unless the tokens alone cannot fill the GPU (64 groups of 16 lanes are
+  // resident on an SM); then they are split into blocks of whole unrolled steps.
   const int steps = (x->heads + norm_rope::kUnroll - 1) / norm_rope::kUnroll;
-  long long want = tokens > 0 ? kGroups / (2 * tokens) : 1;
+  long long want = tokens > 0 ? sm_count() * 64ll / tokens : 1;
   want = std::max(1ll, std::min(want, (long long)steps));
   a->blk = (int)((steps + want - 1) / want) * norm_rope::kUnroll;
   a->n_blk = (x->heads + a->blk - 1) / a->blk;
@@ -554,7 +553,7 @@ struct LinearPlan {
 // launches 6 us and 0.3 us a segment; the plan is the cheapest number of
 // segments under that model (128 (b, h) of 64 chunks: one segment each; 32 of
 // 128 chunks: four, 187 us against 202 us in nine; 15 of 8 chunks: eight, 18 us
-// against 23 us in four).
+// against 23 us in four).  (b, h) x segments past four waves of CTAs gain nothing.
 int linear_plan(int B, int T, int H, int Dh, LinearPlan* pl) {
   if (B < 0 || T < 0 || H < 0) return RATP_ERR_ARG;
   if (Dh != 64 && Dh != 128) return RATP_ERR_SHAPE;
