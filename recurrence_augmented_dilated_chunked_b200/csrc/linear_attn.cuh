@@ -81,7 +81,8 @@ __device__ __forceinline__ float decay_power(float log_decay, double n) { return
 
 // The same to twice the bits, for what a state is multiplied by again and again:
 // a rounding of the power alone would drift the state by as many of its roundings
-// as there are chunks (or decode tokens) within the decay's reach.
+// as there are segments or tokens within the decay's reach (the chunks of a
+// segment spread the low part over their powers, see update).
 struct Decay {
   float hi, lo;
   __device__ __forceinline__ float step(float s, float add) const { return fmaf(hi, s, fmaf(lo, s, add)); }
@@ -590,10 +591,17 @@ __device__ __forceinline__ bool chunk_pass(const CUtensorMap& tm_q, const CUtens
       asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
       mbar_arrive(b_s);
     };
+    float left = 0.f;
     // S = a^n S + chunk c's products, which are done
     auto update = [&](int c) {
       tc_fence_after();
       const Decay a = s_decay[tokens(c) == C ? 0 : 1];
+      // a^n rounded so that what the roundings of the chunks so far have left out
+      // is made up for: their product stays within one rounding of the power
+      left = __fadd_rn(left, a.lo);
+      const float m = __fadd_rn(a.hi, left);
+      left = __fsub_rn(left, __fsub_rn(m, a.hi));
+      const float2 power = make_float2(m, m);
       const uint32_t tc = tl + (OUT ? kColS : (uint32_t)(c & 1) * 128u);
       if (mine) {
 #pragma unroll
@@ -602,7 +610,13 @@ __device__ __forceinline__ bool chunk_pass(const CUtensorMap& tm_q, const CUtens
           tmem_ld32(tc + 32 * q, v);
           tmem_wait_ld();
 #pragma unroll
-          for (int x = 0; x < 32; ++x) S[32 * q + x] = a.step(S[32 * q + x], __uint_as_float(v[x]));
+          for (int x = 0; x < 32; x += 2) {
+            float* s = S + 32 * q + x;
+            const float2 was = make_float2(s[0], s[1]), add = make_float2(__uint_as_float(v[x]), __uint_as_float(v[x + 1]));
+            const float2 y = fma2(power, was, add);
+            s[0] = y.x;
+            s[1] = y.y;
+          }
         }
       }
       tc_fence_before();
