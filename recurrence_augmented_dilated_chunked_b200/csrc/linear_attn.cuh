@@ -54,8 +54,10 @@
 // beside it the scaling of K, its products and S.  One CTA has all of an SM's TMEM
 // and shared memory, so little else hides the chain's latencies: 3.6 us a chunk,
 // 1.4 times its share of the memory's time.  4 x 8192 x 32 x 128 (128 CTAs): 240 us
-// of 165; 2 x 16384 x 16 x 128 (four segments, K and V read twice): 196 us of 82.
-// Scaling that runs a chunk ahead, with six slots: 268 to 292 us for the first.
+// of 165, and 284 us in a run of a second, whose clock the power limit holds at 1.5
+// GHz; 2 x 16384 x 16 x 128 (four segments, K and V read twice): 196 and 217 us of
+// 82.  Scaling that ran a chunk ahead, with six slots, took 268 to 292 us in place of
+// 246 for the first.
 #pragma once
 #include "sm100.cuh"
 
@@ -466,7 +468,7 @@ __device__ __forceinline__ bool chunk_pass(const CUtensorMap& tm_q, const CUtens
         if (!warp_all(mbar_wait(b_qs, (uint32_t)c & 1u, s_abort))) return false;
         tc_fence_after();
         const float2 a2 = make_float2(ai, ai);
-#pragma unroll 2
+#pragma unroll 1
         for (int q = 0; q < DH / 32; ++q) {
           uint32_t r[32];
           tmem_ld32(tl + kColO + 32 * q, r);
