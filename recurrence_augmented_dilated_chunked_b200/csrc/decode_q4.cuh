@@ -38,10 +38,11 @@
 // Ring rows are bf16 already and go through the same accumulators with
 // weights p.
 // Measured (floors at 6.55 TB/s): 64 sequences x 16 heads of 512 slots and a
-// window of 128, 42.5 us of 23.5; 4 x 32 heads of 8192 slots, 46 us of 25.7.
-// About 8 us are the step's start and end (length, inputs, merge, closing
-// counters); the rest streams at 4.5 TB/s, held by the expansion of the codes as
-// much as by memory (with the products left out the second case took 37 us).
+// window of 128, 39 us of 23.5; 4 x 32 heads of 8192 slots, 46 us of 25.7.  About
+// 10 us are the step's start and end (length, inputs, merge, closing counters);
+// the rest is held by the expansion of the codes as much as by memory (the second
+// case took 43 us without its fetches, 37 us without its products).  Ring rows by
+// 16-byte copies of the lanes: 42 us for the first.
 #pragma once
 #include "common.cuh"
 #include "decode.cuh"
@@ -60,7 +61,7 @@ constexpr int kTile = 16;          // keys per MMA tile
 constexpr int kStep = 32;          // cached rows per warp step
 constexpr int kRingStep = 8;       // ring rows per warp step (their bytes fit the same stage)
 constexpr int kStages = 2;         // steps in flight per warp (20 KB of blocks a CTA)
-constexpr int kCtasPerSm = 8;      // 16 warps of 128 registers
+constexpr int kCtasPerSm = 8;      // 16 warps of 128 registers (with 7 and three stages 49 and 58 us)
 constexpr int kGroup = 32;         // channels per scale
 // A ring key moves 512 bytes where a 4-bit key moves 160: it counts as three
 // when a (b, h)'s keys are split over CTAs.

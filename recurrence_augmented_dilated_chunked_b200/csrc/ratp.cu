@@ -671,7 +671,8 @@ long long split_units(bool dense, int T_max, int D, int W, int kv_bits) {
 constexpr int kDecodeCtasPerSm = 6;
 constexpr int kMinSplitKeys = 128;
 // A 4-bit step: the split whose waves of resident CTAs cost least, a CTA
-// costing its keys and kQ4CtaKeys more (start, merge), in units of 4-bit rows.
+// costing its keys and kQ4CtaKeys more (start, merge), in units of 4-bit rows
+// (4 x 32 heads of 8192 slots: 46 us; 49 us with 1024 more, 64 us with 4096).
 constexpr long long kQ4CtaKeys = 256;
 constexpr int kQ4MaxSplits = 64;
 
