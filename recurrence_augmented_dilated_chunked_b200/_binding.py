@@ -435,7 +435,7 @@ def prefill_fused(q, xk, xv, g, D, W=0, head_mask=None, hk=None, hv=None, out=No
 def _head_view(t, name, dtype, device, shape=None):
     """(shape, packed ratp_view) of a [B, T, H, Dh] or [B, H, Dh] view whose
     channels are contiguous."""
-    if not isinstance(t, torch.Tensor) or not t.is_cuda:
+    if not isinstance(t, torch.Tensor):
         raise ValueError("%s must be a CUDA tensor" % name)
     if t.dtype != dtype or t.get_device() != device:
         raise ValueError("%s must be %s on cuda:%d, got %s on %s" % (name, dtype, device, t.dtype, t.device))
@@ -462,6 +462,17 @@ def _new_head_view(like, sz):
 
 
 _NO_VIEW = _VIEW.pack(0, 0, 0, 0, 0, 0)
+
+
+def _vector(t, name, n, device):
+    """Address of a contiguous fp32 [n] tensor (n None: of any length), or None."""
+    if t is None:
+        return None
+    if isinstance(t, torch.Tensor) and t.dtype == torch.float32 and t.get_device() == device and t.is_contiguous():
+        sz = t.shape
+        if len(sz) == 1 and (n is None or sz[0] == n):
+            return t.data_ptr()
+    raise ValueError("%s must be a contiguous fp32 [%s] tensor on cuda:%d" % (name, "rot / 2" if n is None else n, device))
 
 
 def qk_norm_rope(q, k, q_weight, k_weight, inv_freq, positions=None, eps=1e-6, interleaved=False,
@@ -500,7 +511,8 @@ def qk_norm_rope(q, k, q_weight, k_weight, inv_freq, positions=None, eps=1e-6, i
         q_out = q_weight = None
     if k is not None:
         ks, kv = _head_view(k, "k", dt, dev)
-        if q is not None and (len(ks) != len(shape) or ks[:-2] != shape[:-2] or ks[-1] != shape[-1]):
+        if q is not None and (len(ks) != len(shape) or ks[0] != shape[0] or ks[-1] != shape[-1] or
+                              (len(ks) == 4 and ks[1] != shape[1])):
             raise ValueError("q and k must agree in batch, tokens and head size")
         shape = ks
         if k_out is None:
@@ -510,22 +522,18 @@ def qk_norm_rope(q, k, q_weight, k_weight, inv_freq, positions=None, eps=1e-6, i
     else:
         k_out = k_weight = None
     B, T, Dh = shape[0], shape[1] if len(shape) == 4 else 1, shape[-1]
-    for w, nm, n in ((q_weight, "q_weight", Dh), (k_weight, "k_weight", Dh), (inv_freq, "inv_freq", None)):
-        if w is not None:
-            _need(w, nm, torch.float32)
-            if w.dim() != 1 or (n is not None and w.numel() != n) or w.get_device() != dev:
-                raise ValueError("%s must be [%s] on cuda:%d" % (nm, "rot / 2" if n is None else "Dh", dev))
-    per_token = 0
+    qw, kw = _vector(q_weight, "q_weight", Dh, dev), _vector(k_weight, "k_weight", Dh, dev)
+    freq, rot = _vector(inv_freq, "inv_freq", None, dev), 0 if inv_freq is None else 2 * inv_freq.shape[0]
+    pos, per_token = None, 0
     if positions is not None:
         _need(positions, "positions", torch.int32)
-        ps = tuple(positions.shape)
+        ps = positions.shape
         if (ps != (B,) and ps != (B, T)) or positions.get_device() != dev:
             raise ValueError("positions must be int32 [B] or [B, T] on cuda:%d" % dev)
-        per_token = len(ps) - 1
+        pos, per_token = positions.data_ptr(), len(ps) - 1
     with _on(dev):
         _check("ratp_qk_norm_rope", lib.ratp_qk_norm_rope(
-            qv, kv, qo, ko, _addr(q_weight), _addr(k_weight), _addr(inv_freq), _addr(positions), per_token, B, T, Dh,
-            0 if inv_freq is None else 2 * inv_freq.numel(), 1 if interleaved else 0, eps, code, _stream(ref)))
+            qv, kv, qo, ko, qw, kw, freq, pos, per_token, B, T, Dh, rot, 1 if interleaved else 0, eps, code, _stream(ref)))
     return q_out, k_out
 
 
