@@ -27,7 +27,9 @@
 // A sequence is a chain over its chunks, so few (b, h) leave SMs idle: then
 // the chunks are cut into segments.  chunk_kernel<DH, false> computes every
 // segment's own state (from zero), combine_kernel turns those into the state
-// before each segment, and chunk_kernel<DH, true> runs all segments at once.
+// before each segment, and chunk_kernel<DH, true> runs all segments at once.  The
+// three are programmatic dependents: each starts beside the end of the one before
+// and waits for it where it reads a state.
 //
 // Roles of chunk_kernel (448 threads, one CTA per SM):
 //   warps 0-3   P: read Q K^T from TMEM, mask, decay, write bf16 P to TMEM over
@@ -572,6 +574,7 @@ __device__ __forceinline__ bool chunk_pass(const CUtensorMap& tm_q, const CUtens
     const float* src = nullptr;                          // the state before this segment
     if (OUT) src = p.n_seg > 1 ? p.ws + ((size_t)pair * p.n_seg + seg) * DH * DH
                                : p.init != nullptr ? p.init + (size_t)pair * DH * DH : nullptr;
+    if (OUT && p.n_seg > 1) asm volatile("griddepcontrol.wait;" ::: "memory");       // for combine_kernel
     [[maybe_unused]] const long long n_src = (long long)p.B * p.H * p.n_seg * DH * DH;
     const long long at = (long long)r * DH + col0;
     const bool load = mine && src != nullptr && RATP_IN(((long long)pair * p.n_seg + seg) * DH * DH + at, NC, n_src);
@@ -685,6 +688,7 @@ chunk_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ C
   float* s_pow = reinterpret_cast<float*>(smem + L::kOffPow);
   Decay* s_decay = reinterpret_cast<Decay*>(smem + L::kOffDecay);
   uint32_t* s_tmem = reinterpret_cast<uint32_t*>(smem + L::kOffCtl);
+  if (!OUT) asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   const int warp = threadIdx.x >> 5;
   const int per = OUT ? p.n_seg : p.n_seg - 1, pair = blockIdx.x / per;
   if (warp == kMmaWarp) {
@@ -716,8 +720,10 @@ __global__ void __launch_bounds__(256)
 combine_kernel(float* __restrict__ ws, const float* __restrict__ init, const float* __restrict__ log_decay, int H,
                int h0, int n_seg, int quads, int seg_tokens, [[maybe_unused]] long long n_ws) {
   const int e = blockIdx.x * 256 + threadIdx.x, pair = blockIdx.y;
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   if (e >= quads) return;
   const Decay a = decay_pair(log_decay[(h0 + pair) % H], (double)seg_tokens);
+  asm volatile("griddepcontrol.wait;" ::: "memory");
   float4* w = reinterpret_cast<float4*>(ws) + (long long)pair * n_seg * quads + e;
   if (!RATP_IN(((long long)pair * n_seg * quads + e) * 4, ((long long)(n_seg - 1) * quads + 1) * 4, n_ws)) return;
   float4 run = init != nullptr ? reinterpret_cast<const float4*>(init)[(long long)pair * quads + e]

@@ -625,31 +625,48 @@ bool make_chunk_map(CUtensorMap* m, const void* base, int B, int T, int H, int D
             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
+// A launch that may start before the kernel ahead of it has ended (it waits for
+// that itself where it has to).
+template <typename... P, typename... A>
+int launch_early(void (*kernel)(P...), dim3 grid, int threads, int smem, cudaStream_t st, A... args) {
+  cudaLaunchConfig_t cfg;
+  memset(&cfg, 0, sizeof(cfg));
+  cfg.gridDim = grid;
+  cfg.blockDim = dim3(threads);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = st;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, kernel, P(args)...) == cudaSuccess ? launch_status() : RATP_ERR_CUDA;
+}
+
 template <int DH>
 int launch_linear_chunks(const LinearPlan& pl, const CUtensorMap& tq, const CUtensorMap& tk, const CUtensorMap& tv,
-                         const CUtensorMap& to,
-                         const linear_attn::Params& p, cudaStream_t st) {
+                         const CUtensorMap& to, const linear_attn::Params& p, cudaStream_t st) {
   using namespace linear_attn;
   constexpr int smem = (int)Layout<DH>::kBytes;
   const long long pairs = (long long)p.B * p.H;
-  if (pl.n_seg > 1) {
-    if (!ensure_smem(chunk_kernel<DH, false>, smem)) return RATP_ERR_CUDA;
-    chunk_kernel<DH, false><<<(unsigned)(pairs * (pl.n_seg - 1)), kThreads, smem, st>>>(tq, tk, tv, to, p);
-    int rc = launch_status();
-    if (rc) return rc;
-    const int quads = DH * DH / 4;
-    for (long long at = 0; at < pairs; at += 65535) {      // grid.y limit
-      const int n = (int)std::min(65535ll, pairs - at);
-      combine_kernel<<<dim3((unsigned)((quads + 255) / 256), (unsigned)n), 256, 0, st>>>(
-          p.ws + (size_t)at * pl.n_seg * DH * DH, p.init != nullptr ? p.init + (size_t)at * DH * DH : nullptr,
-          p.log_decay, p.H, (int)(at % p.H), pl.n_seg, quads, pl.seg_chunks * C, (pairs - at) * pl.n_seg * DH * DH);
-      rc = launch_status();
-      if (rc) return rc;
-    }
-  }
   if (!ensure_smem(chunk_kernel<DH, true>, smem)) return RATP_ERR_CUDA;
-  chunk_kernel<DH, true><<<(unsigned)(pairs * pl.n_seg), kThreads, smem, st>>>(tq, tk, tv, to, p);
-  return launch_status();
+  if (pl.n_seg == 1) {
+    chunk_kernel<DH, true><<<(unsigned)pairs, kThreads, smem, st>>>(tq, tk, tv, to, p);
+    return launch_status();
+  }
+  if (!ensure_smem(chunk_kernel<DH, false>, smem)) return RATP_ERR_CUDA;
+  chunk_kernel<DH, false><<<(unsigned)(pairs * (pl.n_seg - 1)), kThreads, smem, st>>>(tq, tk, tv, to, p);
+  int rc = launch_status();
+  const int quads = DH * DH / 4;
+  for (long long at = 0; rc == RATP_OK && at < pairs; at += 65535) {       // grid.y limit
+    const int n = (int)std::min(65535ll, pairs - at);
+    rc = launch_early(combine_kernel, dim3((unsigned)((quads + 255) / 256), (unsigned)n), 256, 0, st,
+                      p.ws + (size_t)at * pl.n_seg * DH * DH, p.init != nullptr ? p.init + (size_t)at * DH * DH : nullptr,
+                      p.log_decay, p.H, (int)(at % p.H), pl.n_seg, quads, pl.seg_chunks * C,
+                      (pairs - at) * pl.n_seg * DH * DH);
+  }
+  if (rc != RATP_OK) return rc;
+  return launch_early(chunk_kernel<DH, true>, dim3((unsigned)(pairs * pl.n_seg)), kThreads, smem, st, tq, tk, tv, to, p);
 }
 
 // ---- cache ------------------------------------------------------------------
