@@ -660,8 +660,11 @@ class KVCache:
         n = ctypes.c_size_t()
         _check(size, getattr(lib, size)(B, H, Dh, T_max, D, W, mp, ctypes.byref(n)))
         self.buffer = torch.empty(n.value, dtype=torch.uint8, device=device)
+        if not self.buffer.is_cuda:
+            raise ValueError("a cache lives on a CUDA device, got %s" % self.buffer.device)
+        self._dev = self.buffer.get_device()
         self.c = CacheStruct()
-        with _on(self.buffer.get_device()):
+        with _on(self._dev):
             _check(init, getattr(lib, init)(
                 ctypes.byref(self.c), _ptr(self.buffer), n.value, B, H, Dh, T_max, D, W, mp,
                 _stream(self.buffer)))
@@ -681,8 +684,8 @@ class KVCache:
         """Kc or Vc as [B, rows_per_b, Dh]: bf16, a view of the buffer; for a
         4-bit cache the fp32 values that the held rows stand for."""
         if self.kv_bits == 4:
-            out = torch.empty(self.B, self.c.rows_per_b, self.Dh, dtype=torch.float32, device=self.buffer.device)
-            with _on(out.get_device()):
+            out = self._len.new_empty((self.B, self.c.rows_per_b, self.Dh), dtype=torch.float32)
+            with _on(self._dev):
                 _check("ratp_cache_read_q4", load_library().ratp_cache_read_q4(
                     self._ref, out.data_ptr() if which == "k" else None,
                     None if which == "k" else out.data_ptr(), _stream(out)))
@@ -716,27 +719,30 @@ class KVCache:
             off += cap
         raise IndexError(h)
 
-    def _here(self, t, name, numel, whole=True):
-        """``t`` has the elements that a call reads of it, on the cache's device."""
-        n = t.numel()
-        if n < numel or (whole and n != numel) or t.get_device() != self.buffer.get_device():
-            raise ValueError("%s: %s on %s does not fit the cache (B %d, H %d, Dh %d) on %s" % (
-                name, tuple(t.shape), t.device, self.B, self.H, self.Dh, self.buffer.device))
+    def _fit(self, t, name, dtype, numel, whole=True):
+        """``t`` has what a call reads of it: type, elements, the cache's device."""
+        if (isinstance(t, torch.Tensor) and t.dtype == dtype and t.get_device() == self._dev and t.is_contiguous()):
+            n = t.numel()
+            if n == numel or (n > numel and not whole):
+                return
+        _need(t, name, dtype)
+        raise ValueError("%s: %s on %s does not fit the cache (B %d, H %d, Dh %d) on %s" % (
+            name, tuple(t.shape), t.device, self.B, self.H, self.Dh, self.buffer.device))
 
     def _step_args(self, q, xk, xv, g, state, out):
-        n = self.B * self.H * self.Dh
-        for t, nm in ((q, "q"), (xk, "xk"), (xv, "xv"), (g, "g"), (out, "out")):
-            _need(t, nm, torch.bfloat16)
-            self._here(t, nm, n)
-        _need(state, "state", torch.float32)
-        self._here(state, "state", 2 * n)
+        n, bf16 = self.B * self.H * self.Dh, torch.bfloat16
+        self._fit(q, "q", bf16, n)
+        self._fit(xk, "xk", bf16, n)
+        self._fit(xv, "xv", bf16, n)
+        self._fit(g, "g", bf16, n)
+        self._fit(out, "out", bf16, n)
+        self._fit(state, "state", torch.float32, 2 * n)
 
     def pack(self, hk, hv, T=None):
         _need(hk, "hk", torch.bfloat16)
-        _need(hv, "hv", torch.bfloat16)
         T = hk.shape[1] if T is None else T
         for t, nm in ((hk, "hk"), (hv, "hv")):
-            self._here(t, nm, self.B * int(T) * self.H * self.Dh, whole=False)
+            self._fit(t, nm, torch.bfloat16, self.B * int(T) * self.H * self.Dh, whole=False)
         with _on(hk.get_device()):
             _check("ratp_cache_pack", load_library().ratp_cache_pack(
                 self._ref, _ptr(hk), _ptr(hv), int(T), _stream(hk)))
