@@ -548,8 +548,9 @@ def _linear_args(q, k, v, log_decay, states, out, dims):
         if n and any(isinstance(t, torch.Tensor) and abs(t.data_ptr() - at) < n for t in (q, k, v)):
             raise ValueError("out must not overlap q, k or v")
     for t, nm in ((q, "q"), (k, "k"), (v, "v"), (out, "out")):
-        _need(t, nm, torch.bfloat16)
-        if t.shape != sh or t.get_device() != dev:
+        if not (dev >= 0 and isinstance(t, torch.Tensor) and t.dtype == torch.bfloat16 and t.shape == sh and
+                t.get_device() == dev and t.is_contiguous()):
+            _need(t, nm, torch.bfloat16)
             raise ValueError("q, k, v and out must have one shape, on one device")
     B, H, Dh = sh[0], sh[-2], sh[-1]
     _need(log_decay, "log_decay", torch.float32)
@@ -581,7 +582,7 @@ def linear_attn_prefill(q, k, v, log_decay, initial_state=None, final_state=None
     with _on(q.get_device()):
         if workspace is None:
             n = linear_attn_workspace_bytes(B, T, H, Dh)
-            workspace = torch.empty(n, dtype=torch.uint8, device=q.device) if n else None
+            workspace = q.new_empty(n, dtype=torch.uint8) if n else None
         else:
             _need(workspace, "workspace", torch.uint8)
             if workspace.get_device() != q.get_device():
