@@ -467,6 +467,10 @@ int ratp_cache_init(ratp_cache* c, void* buffer, size_t bytes,
  * Every other entry point takes such a cache as it takes a bf16 one
  * (ratp_cache_pack quantises; ratp_decode_step quantises the row it appends
  * and attends to the held values; ratp_decode_step_layers mixes both kinds).
+ * In the step a weight times a group's step enters the products with 16 bits (two
+ * bf16 parts); scores, sums and the state are fp32, and what the value sums lose
+ * stays below 2^-15 of a step s whatever the number of keys.  Held values up to
+ * 2^100 in magnitude keep the sums finite.
  * Arguments and errors as ratp_cache_bytes / ratp_cache_init. */
 int ratp_cache_bytes_q4(int B, int H, int Dh, int T_max, int D, int W,
                         const uint8_t* head_mask, size_t* bytes);

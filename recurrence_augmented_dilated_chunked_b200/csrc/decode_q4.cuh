@@ -22,23 +22,32 @@
 // only ~28 issue slots per key at the memory rate, and expanding 2 x 128
 // codes in fp32 arithmetic costs about as many.  So the products run as
 // m16n8k16 bf16 MMAs, whose operands are one shift-and-mask per code pair:
-// 0x4300 | n is the bf16 number 128 + n exactly.
+// 0x4180 | n << 3 is the bf16 number 16 + n exactly.
 //   scores  A = 16 keys x 16 channels of codes.  Lane (g, t) of a warp (g =
 //           lane / 4, t = lane % 4) holds keys g and g + 8, channels
 //           [t Dh/4, (t + 1) Dh/4).  B's column n is q restricted to quarter
 //           n of the channels, so C[key][n] are the quarters' separate dot
-//           products, and the score is sum_n s_n C[key][n] + (m_n - 128 s_n)
+//           products, and the score is sum_n s_n C[key][n] + (m_n - 16 s_n)
 //           sum(q in quarter n) (a quarter is one group for Dh = 128, half a
 //           group for Dh = 64).  q enters as it is (bf16), sums are fp32.
 //   values  A = 16 channels x 16 keys of codes (two keys' halves merged by a
 //           byte permute).  B's columns 0..3 are the keys' weights p s of each
 //           quarter, split into a bf16 part (columns 0..3) and the bf16 rest
-//           (columns 4..7), so a weight keeps 16 bits; the offset 128 and the
-//           minima are taken out in fp32 against those same parts.
+//           (columns 4..7), so a weight keeps 16 bits.  A group's values are
+//           m + 7.5 s (its middle, summed in fp32) and s (n - 7.5): the products
+//           sum 16 + n, from which 23.5 times those same parts is taken every
+//           kFold steps.  The sums' roundings go by their size, which is 23.5 p s
+//           a key until then (tensor cores cut them off, always towards zero),
+//           while the output of many keys alike is the small rest of values that
+//           cancel: 256 keys between, at most 2^-23 of the sum lost by each
+//           product, leave 2^-15 of a step s however long the split (128 + n,
+//           taken out at the end only, was off by 1.0% of the output's norm in
+//           splits of 3648 alike keys and by 44% in one of 32768; the rounding of
+//           o is 0.16%).
 // Ring rows are bf16 already and go through the same accumulators with
 // weights p.
 // Measured (floors at 6.55 TB/s): 64 sequences x 16 heads of 512 slots and a
-// window of 128, 39 us of 23.5; 4 x 32 heads of 8192 slots, 46 us of 25.7.  About
+// window of 128, 39.5 us of 23.5; 4 x 32 heads of 8192 slots, 47 us of 25.7.  About
 // 10 us are the step's start and end (length, inputs, merge, closing counters);
 // the rest is held by the expansion of the codes as much as by memory (the second
 // case took 43 us without its fetches, 37 us without its products).  Ring rows by
@@ -325,10 +334,13 @@ __device__ __forceinline__ void mma_bf16(float* c, uint32_t a0, uint32_t a1, uin
       : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
 
-// Code pairs of a word as bf16 pairs 128 + n (channels 2i, 2i + 1).
+// Code pairs of a word as bf16 pairs kOffset + n (channels 2i, 2i + 1).
+constexpr float kOffset = 16.f, kMiddle = 7.5f;
+constexpr int kFold = 8;             // steps between two takings out of the offset: 256 keys of a warp
 __device__ __forceinline__ uint32_t pair_of(uint32_t w, int i) {
+  const uint32_t at = i == 0 ? w << 3 : w >> (4 * i - 3);
   uint32_t r;
-  asm("lop3.b32 %0, %1, %2, %3, 0xea;" : "=r"(r) : "r"(w >> (4 * i)), "r"(0x000f000fu), "r"(0x43004300u));   // (a & b) | c
+  asm("lop3.b32 %0, %1, %2, %3, 0xea;" : "=r"(r) : "r"(at), "r"(0x00780078u), "r"(0x41804180u));   // (a & b) | c
   return r;
 }
 
@@ -364,7 +376,7 @@ constexpr float kSlack = 8.f;
 template <int DH>
 struct Acc {
   float m, l;              // l: this lane's share
-  float zm, zo;            // this lane's column: fp32 sums of w m and of the offset's share
+  float zm, zo;            // this lane's column: fp32 sums of w (m + 7.5 s) and of the parts of w s still offset in c
   float c[DH / 16][4];     // MMA j: channels 2 of this lane's Dh/8 x columns
 };
 
@@ -445,8 +457,8 @@ __device__ __forceinline__ void attend_codes(Acc<DH>& a, const Block<DH>& st, co
       if constexpr (P == 4) read_words<2>(par, &st.kp[16 * u + g + 8 * r][2 * (t & 1)]);
       else par[0] = par[1] = st.kp[16 * u + g + 8 * r][t & 1];
       const float sa = param_scale(par[0]), sb = param_scale(par[1]);
-      float x = fmaf(sa, fmaf(-128.f, qsum[0], d[2 * r]), param_min(par[0]) * qsum[0]);
-      x += fmaf(sb, fmaf(-128.f, qsum[1], d[2 * r + 1]), param_min(par[1]) * qsum[1]);
+      float x = fmaf(sa, fmaf(-kOffset, qsum[0], d[2 * r]), param_min(par[0]) * qsum[0]);
+      x += fmaf(sb, fmaf(-kOffset, qsum[1], d[2 * r + 1]), param_min(par[1]) * qsum[1]);
       x += __shfl_xor_sync(0xffffffffu, x, 1);
       s[2 * u + r] = __shfl_sync(0xffffffffu, x, 0, 4) * scale_log2;
     }
@@ -466,7 +478,7 @@ __device__ __forceinline__ void attend_codes(Acc<DH>& a, const Block<DH>& st, co
     for (int j = 0; j < 4; ++j) {
       const uint32_t par = st.vp[16 * u + 4 * j + t][(g & 3) * P / 4];
       x[j] = pw[j] * param_scale(par);
-      a.zm = fmaf(pw[j], param_min(par), a.zm);
+      a.zm = fmaf(pw[j], fmaf(kMiddle, param_scale(par), param_min(par)), a.zm);
     }
     uint32_t bw[2];
     split_weights(x, rest, bw, &got);
@@ -484,6 +496,20 @@ __device__ __forceinline__ void attend_codes(Acc<DH>& a, const Block<DH>& st, co
         mma_bf16(a.c[4 * w + i], pair_of(l01, i), pair_of(h01, i), pair_of(l23, i), pair_of(h23, i), bw[0], bw[1]);
     }
   }
+}
+
+// Takes the offset of the codes multiplied so far out of the values' sums.
+template <int DH>
+__device__ __forceinline__ void take_offset(Acc<DH>& a, int t) {
+  float z = a.zo;                              // of column g, over this lane's keys
+  z += __shfl_xor_sync(0xffffffffu, z, 1);
+  z += __shfl_xor_sync(0xffffffffu, z, 2);
+  const float z0 = __shfl_sync(0xffffffffu, z, 8 * t), z1 = __shfl_sync(0xffffffffu, z, 8 * t + 4);   // columns 2t, 2t + 1
+#pragma unroll
+  for (int j = 0; j < DH / 16; ++j)
+#pragma unroll
+    for (int i = 0; i < 4; ++i) a.c[j][i] = fmaf(-(kOffset + kMiddle), i & 1 ? z1 : z0, a.c[j][i]);
+  a.zo = 0.f;
 }
 
 // ---- ring rows: bf16, kRingStep of them in a stage ------------------------------
@@ -724,6 +750,7 @@ decode_kernel(const Params pp) {
       phase ^= use == 0 ? 1u : 0u;
     };
     int k = k0, r = r_begin + warp * kRingStep;
+    int folded = 0;                            // steps since the offset was taken out
     for (; k < s_end; k += kRows) {
       fetch_next();
       if (!landed()) break;
@@ -734,6 +761,10 @@ decode_kernel(const Params pp) {
         __syncwarp();
       }
       attend_codes<DH>(a, stages[use], qf, qsum, p.scale_log2, s_end - k, g, tq);
+      if (++folded == kFold) {
+        take_offset<DH>(a, tq);
+        folded = 0;
+      }
       next();
     }
     for (; k >= s_end && r < r_end; r += kWarps * kRingStep) {
@@ -758,8 +789,8 @@ decode_kernel(const Params pp) {
     // ---- this warp's entry ----
 #pragma unroll
     for (int off = 4; off < 32; off <<= 1) a.l += __shfl_xor_sync(0xffffffffu, a.l, off);
-    // minima count once (columns 0..3); the offsets of both parts
-    float z = fmaf(-128.f, a.zo, g < 4 ? a.zm : 0.f);
+    // middles count once (columns 0..3); the offsets of both parts
+    float z = fmaf(-(kOffset + kMiddle), a.zo, g < 4 ? a.zm : 0.f);
     z += __shfl_xor_sync(0xffffffffu, z, 1);
     z += __shfl_xor_sync(0xffffffffu, z, 2);
     z += __shfl_xor_sync(0xffffffffu, z, 16);                      // lanes g and g + 4: quarter g % 4
