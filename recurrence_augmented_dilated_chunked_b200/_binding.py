@@ -739,14 +739,29 @@ class KVCache:
         self._fit(out, "out", bf16, n)
         self._fit(state, "state", torch.float32, 2 * n)
 
+    def _prompt(self, t, name, T):
+        """What a hand-off of T tokens reads of ``t``, dense [B, T, H, Dh].  A
+        tensor of more sequences or tokens (its first two dimensions, with H * Dh
+        elements in the rest) gives the first T tokens of its first B sequences;
+        any other, its first elements."""
+        row = self.H * self.Dh
+        if isinstance(t, torch.Tensor) and t.dim() > 2:
+            n, m = t.shape[:2]
+            if n * m * row == t.numel() and n >= self.B and m > T > 0 and t.is_contiguous():
+                t = t[:self.B, :T].contiguous()        # no copy where B is 1
+        self._fit(t, name, torch.bfloat16, self.B * T * row, whole=False)
+        return t
+
     def pack(self, hk, hv, T=None):
+        """Prefill -> cache hand-off of the first T tokens (default: all) of hk
+        and hv, bf16 [B, >= T, H, Dh]; T below their own length copies those
+        tokens out first where B > 1."""
         _need(hk, "hk", torch.bfloat16)
-        T = hk.shape[1] if T is None else T
-        for t, nm in ((hk, "hk"), (hv, "hv")):
-            self._fit(t, nm, torch.bfloat16, self.B * int(T) * self.H * self.Dh, whole=False)
-        with _on(hk.get_device()):
+        T = int(hk.shape[1] if T is None else T)
+        hk, hv = self._prompt(hk, "hk", T), self._prompt(hv, "hv", T)
+        with _on(self._dev):
             _check("ratp_cache_pack", load_library().ratp_cache_pack(
-                self._ref, _ptr(hk), _ptr(hv), int(T), _stream(hk)))
+                self._ref, _ptr(hk), _ptr(hv), T, _stream(hk)))
 
     def attach_window(self, L):
         """Continue a fixed look-back recurrence of window L at decode: keeps a
@@ -760,12 +775,14 @@ class KVCache:
             ctypes.byref(self.c), _ptr(self.in_ring), n.value, int(L)))
 
     def pack_inputs(self, xk, xv, g, T=None):
-        """Prefill -> decode hand-off of the look-back inputs (last L positions)."""
-        for t, nm in ((xk, "xk"), (xv, "xv"), (g, "g")):
-            _need(t, nm, torch.bfloat16)
-        T = xk.shape[1] if T is None else T
-        _check("ratp_cache_pack_inputs", load_library().ratp_cache_pack_inputs(
-            ctypes.byref(self.c), _ptr(xk), _ptr(xv), _ptr(g), int(T), _stream(xk)))
+        """Prefill -> decode hand-off of the look-back inputs (last L positions
+        before T); tensors as for ``pack``."""
+        _need(xk, "xk", torch.bfloat16)
+        T = int(xk.shape[1] if T is None else T)
+        xk, xv, g = self._prompt(xk, "xk", T), self._prompt(xv, "xv", T), self._prompt(g, "g", T)
+        with _on(self._dev):
+            _check("ratp_cache_pack_inputs", load_library().ratp_cache_pack_inputs(
+                self._ref, _ptr(xk), _ptr(xv), _ptr(g), T, _stream(xk)))
 
     def decode_step(self, q, xk, xv, g, state, out=None):
         """One token per sequence; state: fp32 [2, B, H, Dh] updated in place."""
