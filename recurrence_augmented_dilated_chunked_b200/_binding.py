@@ -720,12 +720,12 @@ class KVCache:
             off += cap
         raise IndexError(h)
 
-    def _fit(self, t, name, dtype, numel, whole=True):
-        """``t`` has what a call reads of it: type, elements, the cache's device."""
-        if (isinstance(t, torch.Tensor) and t.dtype == dtype and t.get_device() == self._dev and t.is_contiguous()):
-            n = t.numel()
-            if n == numel or (n > numel and not whole):
-                return
+    def _fit(self, t, name, dtype, numel):
+        """``t`` has what a call reads of it: type, elements (its front, if it
+        has more), the cache's device."""
+        if (isinstance(t, torch.Tensor) and t.dtype == dtype and t.get_device() == self._dev and t.is_contiguous() and
+                t.numel() >= numel):
+            return
         _need(t, name, dtype)
         raise ValueError("%s: %s on %s does not fit the cache (B %d, H %d, Dh %d) on %s" % (
             name, tuple(t.shape), t.device, self.B, self.H, self.Dh, self.buffer.device))
@@ -738,6 +738,10 @@ class KVCache:
         self._fit(g, "g", bf16, n)
         self._fit(out, "out", bf16, n)
         self._fit(state, "state", torch.float32, 2 * n)
+        # a larger buffer whose front is the state is taken; a state of another
+        # batch is not, since its value stream does not begin where this one's does
+        if state.numel() > 2 * n and state.dim() in (3, 4) and state.shape[0] == 2:
+            raise ValueError("state: %s is not the state of a batch of %d" % (tuple(state.shape), self.B))
 
     def _prompt(self, t, name, T):
         """What a hand-off of T tokens reads of ``t``, dense [B, T, H, Dh].  A
@@ -749,7 +753,7 @@ class KVCache:
             n, m = t.shape[:2]
             if n * m * row == t.numel() and n >= self.B and m > T > 0 and t.is_contiguous():
                 t = t[:self.B, :T].contiguous()        # no copy where B is 1
-        self._fit(t, name, torch.bfloat16, self.B * T * row, whole=False)
+        self._fit(t, name, torch.bfloat16, self.B * T * row)
         return t
 
     def pack(self, hk, hv, T=None):
@@ -785,7 +789,9 @@ class KVCache:
                 self._ref, _ptr(xk), _ptr(xv), _ptr(g), T, _stream(xk)))
 
     def decode_step(self, q, xk, xv, g, state, out=None):
-        """One token per sequence; state: fp32 [2, B, H, Dh] updated in place."""
+        """One token per sequence: q, xk, xv, g, out bf16 [B, H, Dh]; state: fp32
+        [2, B, H, Dh] updated in place.  Of a larger contiguous tensor (a batch
+        padded at its end) the front is used; the rest of out is not written."""
         if out is None and isinstance(q, torch.Tensor):
             out = torch.empty_like(q)
         self._step_args(q, xk, xv, g, state, out)
