@@ -339,15 +339,16 @@ int ratp_dilated_attn_prefill_per_sample_ws(const void* q, const void* hk, const
  *   are not negative, and keep every row 16-byte aligned (so q and k may be
  *   read out of one fused projection).  A decode token is T = 1.  An output
  *   view may be the input view itself (same data and strides: in place);
- *   otherwise outputs overlap neither inputs nor each other.  A tensor with
- *   heads == 0 is left out.
+ *   otherwise outputs share no element with an input or with each other
+ *   (interleaved rows of one buffer do not).  A tensor with heads == 0 is left
+ *   out.
  * q_weight, k_weight: fp32 [Dh] gains; NULL = 1.
  * inv_freq: fp32 [rot/2]; may be NULL when rot == 0 (norm only).
  * positions: NULL (token t sits at position t); int32 [B] (position of token
  *   0 of each sequence, e.g. a cache's len: token t sits at positions[b] + t);
  *   or int32 [B][T] with positions_per_token != 0.  Any int32 value.
  * Errors: ARG (null pointer, negative size or stride, an output whose own rows
- *   overlap, bad dtype, eps < 0 or not finite), SHAPE (Dh not 64/128, rot not a multiple of 16 in 0..Dh, too
+ *   overlap or that shares elements with another tensor, bad dtype, eps < 0 or not finite), SHAPE (Dh not 64/128, rot not a multiple of 16 in 0..Dh, too
  *   many heads), ALIGN.  B or T == 0 is a no-op.
  * ---------------------------------------------------------------------- */
 typedef struct ratp_view {

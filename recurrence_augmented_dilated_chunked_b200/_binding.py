@@ -491,7 +491,8 @@ def qk_norm_rope(q, k, q_weight, k_weight, inv_freq, positions=None, eps=1e-6, i
     with ``interleaved``.
     positions: None (0 .. T-1), int32 [B] (the position of each sequence's
     first token here, e.g. ``KVCache.lengths()``) or int32 [B, T].
-    q_out, k_out: outputs; q and k themselves work in place."""
+    q_out, k_out: outputs; q and k themselves work in place, otherwise outputs
+    share no element with q, k or each other."""
     lib = load_library()
     ref = k if q is None else q
     if not isinstance(ref, torch.Tensor) or not ref.is_cuda:

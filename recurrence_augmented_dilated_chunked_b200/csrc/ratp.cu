@@ -42,6 +42,7 @@ __global__ void guard_probe_kernel() {
 #include "decode_q4.cuh"
 #include "norm_rope.cuh"
 #include "linear_attn.cuh"
+#include "overlap.h"
 
 using namespace ratp;
 
@@ -1220,6 +1221,14 @@ int ratp_qk_norm_rope(const ratp_view* q, const ratp_view* k, const ratp_view* q
     p.units += n;
   }
   if (!aligned16(inv_freq) || (reinterpret_cast<uintptr_t>(positions) & 3u) != 0) return RATP_ERR_ALIGN;
+  // an output is its own input or shares nothing with any other tensor
+  for (int i = 0; i < 2; ++i) {
+    if (in[i]->heads == 0) continue;
+    for (int j = 0; j < 2; ++j)
+      if (in[j]->heads > 0 && !(i == j && same_rows(*out[i], *in[i], B, T)) && views_overlap(*out[i], *in[j], esize, B, T, Dh))
+        return RATP_ERR_ARG;
+  }
+  if (in[0]->heads > 0 && in[1]->heads > 0 && views_overlap(*out[0], *out[1], esize, B, T, Dh)) return RATP_ERR_ARG;
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   return dtype == RATP_BF16 ? launch_norm_rope<__nv_bfloat16>(p, Dh, st) : launch_norm_rope<float>(p, Dh, st);
 }
