@@ -371,7 +371,8 @@ int ratp_qk_norm_rope(const ratp_view* q, const ratp_view* k, const ratp_view* q
  *   o_t = scale * q_t S_t
  *
  * q, k, v, o: bf16 [B][T][H][Dh] (step: [B][H][Dh]), Dh 64 or 128.
- *   o overlaps none of the others.
+ *   o, final_state and workspace overlap each other and the inputs nowhere
+ *   (final_state may be initial_state itself).
  * log_decay: fp32 [H], values <= 0 (0: no decay; -inf: no memory); a kernel
  *   that reads another value or a NaN records ARG (ratp_last_error).
  * A value of v that is not finite makes its channel of o NaN from its token on,
@@ -387,8 +388,8 @@ int ratp_qk_norm_rope(const ratp_view* q, const ratp_view* k, const ratp_view* q
  *   the (b, h) alone fill the GPU), 16-byte aligned, no initialisation; calls
  *   sharing one must be ordered on one stream.
  * ratp_linear_attn_step: one token per sequence, state updated in place.
- * Errors: ARG (null pointer, negative size, scale not finite), SHAPE (Dh, H *
- *   B * tokens too large), ALIGN, CAPACITY (workspace too small), UNSUPPORTED
+ * Errors: ARG (null pointer, negative size, scale not finite, tensors that
+ *   overlap), SHAPE (Dh, H * B * tokens too large), ALIGN, CAPACITY (workspace too small), UNSUPPORTED
  *   (dtype not bf16).  B or H == 0 is a no-op; T == 0 hands the initial state
  *   on to final_state.
  * ---------------------------------------------------------------------- */

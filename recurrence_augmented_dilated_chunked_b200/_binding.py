@@ -572,8 +572,8 @@ def linear_attn_prefill(q, k, v, log_decay, initial_state=None, final_state=None
 
     log_decay: fp32 [H], <= 0.  initial_state: fp32 [B, H, Dh, Dh] before the
     first token (None: zero); final_state: receives the state after the last
-    one, and may be initial_state itself.  scale: Dh ** -0.5 by default.
-    out: must not overlap q, k or v.
+    one, and may be initial_state itself, but not overlap it in part.  scale:
+    Dh ** -0.5 by default.  out: must not overlap q, k, v or a state.
     workspace: uint8 tensor of ``linear_attn_workspace_bytes`` (default: one
     from the current stream's allocator, so that no two calls or captured
     graphs share one)."""

@@ -596,6 +596,27 @@ int check_linear(const void* q, const void* k, const void* v, const float* ld, c
   return RATP_OK;
 }
 
+// What a call writes shares no byte with what it reads or writes besides, but
+// that the final state may be the initial one itself.
+bool apart(const void* a, size_t an, const void* b, size_t bn) {
+  const uintptr_t x = reinterpret_cast<uintptr_t>(a), y = reinterpret_cast<uintptr_t>(b);
+  return a == nullptr || b == nullptr || x + an <= y || y + bn <= x;
+}
+bool linear_apart(const void* q, const void* k, const void* v, const float* init, const float* fin, const void* o,
+                  const void* ws, size_t ws_bytes, long long tokens, long long pairs, int H, int Dh) {
+  const size_t n = (size_t)tokens * H * Dh * 2, m = (size_t)pairs * Dh * Dh * 4;
+  const void* out[3] = {o, fin, ws};
+  const size_t bytes[3] = {n, m, ws_bytes};
+  for (int i = 0; i < 3; ++i) {
+    for (const void* x : {q, k, v})
+      if (!apart(out[i], bytes[i], x, n)) return false;
+    if (!(i == 1 && fin == init) && !apart(out[i], bytes[i], init, m)) return false;
+    for (int j = 0; j < i; ++j)
+      if (!apart(out[i], bytes[i], out[j], bytes[j])) return false;
+  }
+  return true;
+}
+
 int launch_linear_recurrent(const void* q, const void* k, const void* v, const float* ld, const float* init, float* fin,
                             void* o, int B, int T, int H, int Dh, float scale, cudaStream_t st) {
   linear_attn::RecurrentParams p;
@@ -1139,6 +1160,7 @@ int ratp_linear_attn_prefill(const void* q, const void* k, const void* v, const 
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   if (T == 0 && (long long)B * H > 0 && final_state != nullptr && final_state != initial_state) {
     const size_t n = (size_t)B * H * Dh * Dh * 4;        // no token: the state as it was
+    if (!apart(final_state, n, initial_state, n)) return RATP_ERR_ARG;
     const cudaError_t e = initial_state != nullptr ? cudaMemcpyAsync(final_state, initial_state, n, cudaMemcpyDeviceToDevice, st)
                                                    : cudaMemsetAsync(final_state, 0, n, st);
     return e == cudaSuccess ? RATP_OK : RATP_ERR_CUDA;
@@ -1146,14 +1168,20 @@ int ratp_linear_attn_prefill(const void* q, const void* k, const void* v, const 
   if ((long long)B * T * H == 0) return RATP_OK;
   rc = check_linear(q, k, v, log_decay, initial_state, final_state, o, scale, dtype);
   if (rc) return rc;
-  if (T <= linear_attn::kRecurrentTokens)
+  const auto separate = [&](const void* ws, size_t n) {
+    return linear_apart(q, k, v, initial_state, final_state, o, ws, n, (long long)B * T, (long long)B * H, H, Dh);
+  };
+  if (T <= linear_attn::kRecurrentTokens) {
+    if (!separate(nullptr, 0)) return RATP_ERR_ARG;
     return launch_linear_recurrent(q, k, v, log_decay, initial_state, final_state, o, B, T, H, Dh, scale, st);
+  }
   const size_t need = linear_ws_bytes(pl, B, H, Dh);
   if (need > 0) {
     if (!workspace) return RATP_ERR_ARG;
     if (!aligned16(workspace)) return RATP_ERR_ALIGN;
     if (workspace_bytes < need) return RATP_ERR_CAPACITY;
   }
+  if (!separate(need > 0 ? workspace : nullptr, need)) return RATP_ERR_ARG;
   linear_attn::Params p;
   memset(&p, 0, sizeof(p));
   p.log_decay = log_decay;
@@ -1179,6 +1207,7 @@ int ratp_linear_attn_step(const void* q, const void* k, const void* v, const flo
   if (!state) return RATP_ERR_ARG;
   const int rc = check_linear(q, k, v, log_decay, state, state, o, scale, dtype);
   if (rc) return rc;
+  if (!linear_apart(q, k, v, state, state, o, nullptr, 0, B, (long long)B * H, H, Dh)) return RATP_ERR_ARG;
   return launch_linear_recurrent(q, k, v, log_decay, state, state, o, B, 1, H, Dh, scale,
                                  static_cast<cudaStream_t>(stream));
 }
