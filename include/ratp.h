@@ -376,7 +376,8 @@ int ratp_qk_norm_rope(const ratp_view* q, const ratp_view* k, const ratp_view* q
  * log_decay: fp32 [H], values <= 0 (0: no decay; -inf: no memory); a kernel
  *   that reads another value or a NaN records ARG (ratp_last_error).
  * A value of v that is not finite makes its channel of o NaN from its token on,
- *   as one of k does for all channels; tokens before it are as without it.
+ *   as one of k does for all channels; tokens before it are as without it.  An
+ *   infinite entry of a state stays infinite while the decay's power is above 0.
  * initial_state: fp32 [B][H][Dh][Dh] (row: channel of k, column: channel of v)
  *   before the first token; NULL = zero.  final_state: the state after the
  *   last token, or NULL; it may be initial_state itself (in place).  A prefill

@@ -87,9 +87,14 @@ __device__ __forceinline__ float decay_power(float log_decay, double n) { return
 // a rounding of the power alone would drift the state by as many of its roundings
 // as there are segments or tokens within the decay's reach (the chunks of a
 // segment spread the low part over their powers, see update).
+// An infinite state stays what it is: the low part, which may be negative or zero,
+// is multiplied by the largest finite number in its place.
 struct Decay {
   float hi, lo;
-  __device__ __forceinline__ float step(float s, float add) const { return fmaf(hi, s, fmaf(lo, s, add)); }
+  __device__ __forceinline__ float step(float s, float add) const {
+    constexpr float kMost = 3.402823466e38f;
+    return fmaf(hi, s, fmaf(lo, fminf(fmaxf(s, -kMost), kMost), add));
+  }
 };
 __device__ __forceinline__ Decay decay_pair(float log_decay, double n) {
   const double x = exact_power(log_decay, n);
