@@ -710,10 +710,16 @@ long long split_units(bool dense, int T_max, int D, int W, int kv_bits) {
 constexpr int kDecodeCtasPerSm = 6;
 constexpr int kMinSplitKeys = 128;
 // A 4-bit step: the split whose waves of resident CTAs cost least, a CTA
-// costing its keys and kQ4CtaKeys more (start, merge), in units of 4-bit rows
-// (4 x 32 heads of 8192 slots: 46 us; 49 us with 1024 more, 64 us with 4096).
-constexpr long long kQ4CtaKeys = 256;
-constexpr int kQ4MaxSplits = 64;
+// costing its keys and kQ4CtaKeys more (start, merge), and each split of a head
+// past kQ4FreeSplits kQ4MergeKeys (the last split reads the partials one after the
+// other), in units of 4-bit rows.  Measured: 4 x 32 heads of 8192 slots 46 us, 49
+// us with 1024 in place of 256, 64 us with 4096.  One head of 1M slots: 239, 139,
+// 121, 148 and 231 us in 64, 128, 169 (the model's), 256 and 1024 splits, 217 us in
+// bf16; one of 256K slots: 72, 64, 55, 73 and 204 us in 64, 82 (the model's), 128,
+// 256 and 1024; four of 128K slots: 64, 67 and 72 us in 64 (the model's), 82 and
+// 256; sixteen of 32K slots: 36, 37 and 42 us in 64 (the model's), 74 and 41.
+constexpr long long kQ4CtaKeys = 256, kQ4FreeSplits = 64, kQ4MergeKeys = 32;
+constexpr int kQ4MaxSplits = 256;
 
 // Blocks of one batch item of a 4-bit cache, and a block's bytes.
 long long q4_blocks_per_b(int H, int T_max, int D, const uint8_t* dense) {
@@ -734,7 +740,8 @@ long long q4_split(int B, int H, int T_max, int D, int W, const uint8_t* head_ma
       const long long keys = split_units(head_mask != nullptr && head_mask[h] != 0, T_max, D, W, 4);
       ctas += std::max(1ll, (keys + split - 1) / std::max(split, 1ll));
     }
-    const long long cost = (ctas * B + slots - 1) / slots * (split + kQ4CtaKeys);
+    const long long merged = std::max(0ll, (max_keys + split - 1) / std::max(split, 1ll) - kQ4FreeSplits);
+    const long long cost = (ctas * B + slots - 1) / slots * (split + kQ4CtaKeys) + kQ4MergeKeys * merged;
     if (n == 1 || cost < best_cost) { best = std::max(split, (long long)decode_q4::kStep); best_cost = cost; }
   }
   return best;

@@ -44,6 +44,7 @@ def reference(cache, q, state):
     (1, 2, 65536, True),       # one split: 32768 keys a warp
     (1, 1, 65536, False),      # as the cache splits it
     (4, 16, 32768, False),
+    (1, 1, 1 << 20, False),    # as many splits as a head can have
 ])
 def test_alike_keys(B, H, T, whole, Dh):
     gen = torch.Generator(device=DEV).manual_seed(T + Dh)
