@@ -162,7 +162,9 @@ norm_rope_kernel(const Params p) {
 #pragma unroll
     for (int i = 0; i < kUnroll; ++i) {
       if (h + i >= h1) continue;
-      const float r = rsqrtf(ss[i] * (1.f / DH) + p.eps);
+      // fp32 outputs keep the root's last bits; bf16 has no place for them
+      const float ms = ss[i] * (1.f / DH) + p.eps;
+      const float r = sizeof(E) == 4 ? __frsqrt_rn(ms) : rsqrtf(ms);
       float oa[4], ob[4];
 #pragma unroll
       for (int j = 0; j < 4; ++j) {
