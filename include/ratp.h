@@ -456,7 +456,8 @@ int ratp_cache_init(ratp_cache* c, void* buffer, size_t bytes,
  * section 8.2 names low-bit quantisation of the compressed cache as the next
  * step).  Each row is kept in groups of 32 channels; a group keeps its minimum
  * m, the step s = bf16((max - m) / 15) and the codes n = round((x - m) / s) in
- * 0..15 (round half to even; 0 where s == 0), and stands for m + n s, so that
+ * 0..15 (round half to even of the quotient, x - m rounded to fp32; 0 where s ==
+ * 0), and stands for m + n s, so that
  * a row of Dh channels takes Dh/2 + Dh/8 bytes instead of 2 Dh.
  * Layout (Kc): head h keeps its slots in ceil(cap_h / 32) blocks of 32, the
  * heads of a batch item one after the other; a block is uint32 K codes [32]

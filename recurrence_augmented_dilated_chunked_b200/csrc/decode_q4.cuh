@@ -105,8 +105,8 @@ __device__ __forceinline__ float param_scale(uint32_t p) { return __uint_as_floa
 __device__ __forceinline__ float param_min(uint32_t p) { return __uint_as_float(p & 0xffff0000u); }
 
 // ---- quantisation -------------------------------------------------------------
-// Every step rounds as the definition does (to nearest even), so the codes are
-// the definition's.
+// Every step rounds as the definition does (to nearest even; x - m to fp32, the
+// quotient of that by s once, to the code), so the codes are the definition's.
 __device__ __forceinline__ uint32_t group_params(float lo, float hi) {
   // d / 15 correctly rounded: the product's remainder is exact in one fma, and
   // no quotient by 15 lies near enough to a rounding boundary to be missed
