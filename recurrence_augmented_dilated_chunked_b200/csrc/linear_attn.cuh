@@ -59,7 +59,9 @@
 // of 165, and 284 us in a run of a second, whose clock the power limit holds at 1.5
 // GHz; 2 x 16384 x 16 x 128 (four segments, K and V read twice): 196 and 217 us of
 // 82.  Scaling that ran a chunk ahead, with six slots, took 268 to 292 us in place of
-// 246 for the first.
+// 246 for the first.  For Dh = 64 the chain is nearly as long on half the bytes:
+// 4 x 8192 x 32 x 64 in 167 us (176 in a run) of 82.  At 128 registers chunk_kernel<128, true> spills
+// 48 bytes and loads 52 a thread, <64, true> 32 and 68 (the repair pass 80 and 168).
 #pragma once
 #include "sm100.cuh"
 
@@ -74,6 +76,12 @@ constexpr int kMmaWarp = 13;
 constexpr int kSlots = 5;
 constexpr int kPart = 32;               // tokens whose scaled K is handed to the MMA at a time
 constexpr int kParts = C / kPart;
+// Sequences of up to this many tokens run token by token.  Measured, us (token by
+// token / in chunks, states in and out), T = 8, 16, 32:
+//   Dh 128,    4 (b, h):  7.7 / 13.5,  13.3 / 13.5,  24.1 / 13.7
+//   Dh 128, 1024 (b, h): 45.9 / 87.9,  81.7 / 88.3, 158.4 / 90.3
+//   Dh  64,    4 (b, h):  6.1 /  7.8,  10.4 /  7.8,  18.7 /  7.7
+//   Dh  64, 1024 (b, h): 16.4 / 52.8,  28.8 / 52.8,  53.5 / 52.9
 constexpr int kRecurrentTokens = 16;
 
 // a^n for n >= 0 tokens.  log_decay is clamped to a finite value, below which

@@ -554,7 +554,11 @@ struct LinearPlan {
 // launches 6 us and 0.3 us a segment; the plan is the cheapest number of
 // segments under that model (128 (b, h) of 64 chunks: one segment each; 32 of
 // 128 chunks: four, 187 us against 202 us in nine; 15 of 8 chunks: eight, 18 us
-// against 23 us in four).  (b, h) x segments past four waves of CTAs gain nothing.
+// against 23 us in four).  These are for Dh = 128; a chunk of Dh = 64 takes 2.6 us
+// with output, but the ratios hold: 32 of 128 chunks 146 us in four, 147 in nine;
+// 16 of 128 chunks 77 in nine, 100 in six, 87 in sixteen; 15 of 8 chunks 18.4 in
+// eight, 21 in four; 8 of 64 chunks 28.7 in sixteen, 34 in twelve (the model's
+// choice first).  (b, h) x segments past four waves of CTAs gain nothing.
 int linear_plan(int B, int T, int H, int Dh, LinearPlan* pl) {
   if (B < 0 || T < 0 || H < 0) return RATP_ERR_ARG;
   if (Dh != 64 && Dh != 128) return RATP_ERR_SHAPE;
