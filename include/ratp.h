@@ -417,7 +417,7 @@ int ratp_linear_attn_step(const void* q, const void* k, const void* v, const flo
  *          a decode step starts; ratp_cache_init zeroes them and every step
  *          leaves them zero.
  * The struct is plain data filled by ratp_cache_init; the caller owns the
- * buffer it points into.
+ * buffer it points into.  Callers and library are compiled with the same header.
  * ---------------------------------------------------------------------- */
 typedef struct ratp_cache {
   void* Kc;
