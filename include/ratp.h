@@ -532,8 +532,8 @@ int ratp_cache_pack_inputs(ratp_cache* c, const void* xk, const void* xv, const 
  * new key/value itself; len[b] += 1.
  * q, xk, xv, g, o: bf16 [B][H][Dh].  D, W, head_mask must equal the values
  * the cache was initialised with (ERR_ARG otherwise).  A token beyond T_max
- * sets RATP_ERR_CAPACITY in the device error word and leaves that sequence
- * unchanged. */
+ * (or before 0: a length that was written over) sets RATP_ERR_CAPACITY in the
+ * device error word and leaves that sequence unchanged. */
 int ratp_decode_step(const void* q, const void* xk, const void* xv, const void* g,
                      float* state, ratp_cache* c, void* o,
                      int D, int W, const uint8_t* head_mask, void* stream);

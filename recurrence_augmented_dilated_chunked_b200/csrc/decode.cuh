@@ -227,7 +227,7 @@ __device__ __forceinline__ void advance_len(const Params& p, int b) {
     const unsigned int prev = atomicAdd(cnt, 1u);
     if (prev == (unsigned int)p.splits_per_b - 1u) {
       const int tb = p.len[b];
-      if (tb < p.T_max) p.len[b] = tb + 1;
+      if ((unsigned)tb < (unsigned)p.T_max) p.len[b] = tb + 1;
       *cnt = 0u;
     }
   }
@@ -278,7 +278,7 @@ decode_kernel(const Params p) {
   const int Dd = dense ? 1 : p.D;
   bool active = true;
   int n_slots = 0, w_lo = 0, n_win = 0, n_keys = 0, n_used = 1, app_slot = 0;
-  if (t >= p.T_max) {
+  if ((unsigned)t >= (unsigned)p.T_max) {        // full, or a length that is none
     active = false;
     if (split == 0 && h == 0 && tid == 0) raise_error(RATP_ERR_CAPACITY);
   } else {

@@ -633,7 +633,7 @@ decode_kernel(const Params pp) {
   const int Dd = dense ? 1 : p.D;
   bool active = true;
   int n_slots = 0, w_lo = 0, n_win = 0, n_used = 1, app_slot = 0;
-  if (t >= p.T_max) {
+  if ((unsigned)t >= (unsigned)p.T_max) {      // full, or a length that is none
     active = false;
     if (split == 0 && h == 0 && tid == 0) raise_error(RATP_ERR_CAPACITY);
   } else {

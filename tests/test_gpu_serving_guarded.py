@@ -17,7 +17,8 @@ def test_later_serving_tests_under_the_guarded_build():
     env = dict(os.environ, RATP_LIBRARY=B_.build_library(guarded=True))
     env["PYTHONPATH"] = ROOT + os.pathsep + env.get("PYTHONPATH", "")
     files = ["tests/test_gpu_%s.py" % n for n in ("cache_q4_long", "cache_q4_edges", "cache_handoff", "padded_batch",
-                                                  "norm_rope_f32", "linear_attn_infinite", "linear_attn_state")]
+                                                  "cache_lengths", "norm_rope_f32", "linear_attn_infinite",
+                                                  "linear_attn_state")]
     res = subprocess.run([sys.executable, "-m", "pytest", "-x", "-q", "-m", "gpu", "-p", "no:cacheprovider"] + files,
                          cwd=ROOT, env=env, capture_output=True, text=True, timeout=1200)
     assert res.returncode == 0, "\n".join((res.stdout + res.stderr).splitlines()[-30:])
